@@ -1,0 +1,255 @@
+// linear.hip -- C entry points of the products with 4-bit group-quantized
+// weights (fq_linear.h): argument checks and the choice of a kernel, and the
+// kernel that serves every shape.
+//
+// The kernel: C[i, j] = sum_l A(i, l) B(j, l) in binary32 on a 64 x 64 tile of
+// LDS, 16 sums per thread.  A and B are any functions of two indices (a dense
+// matrix, its transpose, a stored 4-bit matrix, a gradient formed from dh, g, u).
+#include "fq_host.h"
+#include "w4_device.h"
+
+using namespace fqw;
+
+namespace {
+
+constexpr int kTile = 64, kDepth = 16;
+
+template <class T>
+struct Dense {  // element (i, l) of a row-major matrix with row stride ld, or of its transpose
+    const T* p;
+    int64_t si, sl;
+    __device__ __forceinline__ float at(int64_t i, int64_t l) const { return load_f(p + i * si + l * sl); }
+};
+struct W4Rows {
+    W4Mat w;
+    __device__ __forceinline__ float at(int64_t r, int64_t l) const { return w.at(r, l); }
+};
+struct W4Cols {  // [gate | up] columns as rows: (c, l) with l running over both matrices' rows
+    W4Mat a, b;
+    int64_t n;
+    __device__ __forceinline__ float at(int64_t c, int64_t l) const { return l < n ? a.at(l, c) : b.at(l - n, c); }
+};
+struct GateGrad {  // dg (l < n) and du (l >= n) of token i; TR: (l, i)
+    const uint16_t *dh, *g, *u;
+    int64_t n;
+    int act;
+    bool tr;
+    __device__ __forceinline__ float at(int64_t i, int64_t l) const {
+        const int64_t t = tr ? l : i, f = tr ? i : l, c = f < n ? f : f - n;
+        const float d = load_f(dh + t * n + c);
+        float v, s;
+        act_both(act, load_f(g + t * n + c), v, s);
+        return f < n ? d * load_f(u + t * n + c) * s : d * v;
+    }
+};
+
+template <class T>
+struct Store {
+    T *p, *p2;     // rows >= split go to p2
+    int64_t ld, split;
+    __device__ __forceinline__ void put(int64_t i, int64_t j, float v) const {
+        if (i < split) store_f(p + i * ld + j, v);
+        else store_f(p2 + (i - split) * ld + j, v);
+    }
+};
+
+template <class A, class B, class Put>
+__device__ __forceinline__ void tile_sum(const A& a, const B& b, int64_t I, int64_t J, int64_t L, int64_t i0, int64_t j0,
+                                         float (&acc)[4][4], float* sa, float* sb, Put) {
+    const int t = threadIdx.x, ti = t / 16, tj = t % 16;
+    for (int64_t l0 = 0; l0 < L; l0 += kDepth) {
+        for (int e = t; e < kTile * kDepth; e += 256) {
+            const int r = e / kDepth, l = e % kDepth;
+            const bool in = l0 + l < L;
+            sa[l * (kTile + 1) + r] = in && i0 + r < I ? a.at(i0 + r, l0 + l) : 0.0f;
+            sb[l * (kTile + 1) + r] = in && j0 + r < J ? b.at(j0 + r, l0 + l) : 0.0f;
+        }
+        __syncthreads();
+        for (int l = 0; l < kDepth; ++l)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    acc[x][y] = fmaf(sa[l * (kTile + 1) + ti + 16 * x], sb[l * (kTile + 1) + tj + 16 * y], acc[x][y]);
+        __syncthreads();
+    }
+}
+
+template <class A, class B, class Put>
+__global__ __launch_bounds__(256) void k_tile(A a, B b, Put put, int64_t I, int64_t J, int64_t L, int64_t nj) {
+    __shared__ float sa[kDepth * (kTile + 1)], sb[kDepth * (kTile + 1)];
+    const int64_t i0 = blockIdx.x / nj * kTile, j0 = blockIdx.x % nj * kTile;
+    float acc[4][4] = {};
+    tile_sum(a, b, I, J, L, i0, j0, acc, sa, sb, 0);
+    for (int x = 0; x < 4; ++x)
+        for (int y = 0; y < 4; ++y) {
+            const int64_t i = i0 + threadIdx.x / 16 + 16 * x, j = j0 + threadIdx.x % 16 + 16 * y;
+            if (i < I && j < J) put.put(i, j, acc[x][y]);
+        }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_tile_gated(Dense<T> x, W4Rows gate, W4Rows up, T* h, T* g, T* u, int act,
+                                                    int64_t I, int64_t J, int64_t L, int64_t nj) {
+    __shared__ float sa[kDepth * (kTile + 1)], sb[kDepth * (kTile + 1)];
+    const int64_t i0 = blockIdx.x / nj * kTile, j0 = blockIdx.x % nj * kTile;
+    float ga[4][4] = {}, ua[4][4] = {};
+    tile_sum(x, gate, I, J, L, i0, j0, ga, sa, sb, 0);
+    tile_sum(x, up, I, J, L, i0, j0, ua, sa, sb, 0);
+    for (int a = 0; a < 4; ++a)
+        for (int b = 0; b < 4; ++b) {
+            const int64_t i = i0 + threadIdx.x / 16 + 16 * a, j = j0 + threadIdx.x % 16 + 16 * b;
+            if (i >= I || j >= J) continue;
+            store_f(h + i * J + j, act_value(act, ga[a][b]) * ua[a][b]);
+            if (g) {
+                store_f(g + i * J + j, ga[a][b]);
+                store_f(u + i * J + j, ua[a][b]);
+            }
+        }
+}
+
+__global__ __launch_bounds__(256) void k_zero16(uint16_t* p, int64_t n) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0;
+}
+
+// Zeros to `bytes` (a multiple of 2) at p by a kernel (a fill node in a captured
+// graph would not replay reliably).
+void fill_zero(void* p, int64_t bytes, hipStream_t stream) {
+    k_zero16<<<fqh::grid_for(bytes / 2, 256, 16), 256, 0, stream>>>((uint16_t*)p, bytes / 2);
+}
+
+template <class A, class B, class Put>
+int run_tile(const A& a, const B& b, const Put& put, int64_t I, int64_t J, int64_t L, hipStream_t stream) {
+    const int64_t ni = (I + kTile - 1) / kTile, nj = (J + kTile - 1) / kTile;
+    if (ni * nj > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
+    k_tile<<<(unsigned)(ni * nj), 256, 0, stream>>>(a, b, put, I, J, L, nj);
+    return fqh::launched();
+}
+
+bool valid_sizes(int64_t m, int64_t n, int64_t k, int64_t group) {
+    constexpr int64_t kMax = (int64_t)1 << 31;
+    return m >= 0 && n >= 1 && k >= 1 && group >= 1 && m < kMax && n < kMax && k < kMax;
+}
+bool valid_weight(const fql_w4* w) {
+    return w && w->codes && w->scale && fqh::aligned(w->scale, 4) && fqh::aligned(w->zero_point, 4);
+}
+uintptr_t elem(int dtype) { return dtype == FQ_F32 ? 4 : 2; }
+
+template <class T>
+int matmul(const void* x, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4& w, void* y, hipStream_t stream) {
+    return run_tile(Dense<T>{(const T*)x, k, 1}, W4Rows{w4_mat(w, k, group)}, Store<T>{(T*)y, nullptr, n, m}, m, n, k,
+                    stream);
+}
+
+template <class T>
+int gated(const void* x, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4& gate, const fql_w4& up,
+          void* h, void* g, void* u, hipStream_t stream) {
+    const int64_t ni = (m + kTile - 1) / kTile, nj = (n + kTile - 1) / kTile;
+    if (ni * nj > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
+    k_tile_gated<T><<<(unsigned)(ni * nj), 256, 0, stream>>>(Dense<T>{(const T*)x, k, 1}, W4Rows{w4_mat(gate, k, group)},
+                                                             W4Rows{w4_mat(up, k, group)}, (T*)h, (T*)g, (T*)u, act, m,
+                                                             n, k, nj);
+    return fqh::launched();
+}
+
+template <class A>
+int grad_weight(const A& a, const void* x, int64_t m, int64_t rows, int64_t n, int64_t k, void* dw, void* dw2,
+                int dw_dtype, hipStream_t stream) {
+    const Dense<uint16_t> xt{(const uint16_t*)x, 1, k};
+    return dw_dtype == FQ_F32
+               ? run_tile(a, xt, Store<float>{(float*)dw, (float*)dw2, k, n}, rows, k, m, stream)
+               : run_tile(a, xt, Store<uint16_t>{(uint16_t*)dw, (uint16_t*)dw2, k, n}, rows, k, m, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fql_w4_matmul_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t fql_w4_gated_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t fql_w4_matmul_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t fql_w4_gated_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4* w, void* y,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!fqh::valid_dtype(dtype)) return FQ_E_UNSUPPORTED;
+    if (!valid_sizes(m, n, k, group) || !valid_weight(w)) return FQ_E_INVALID;
+    if (m == 0) return FQ_OK;
+    if (!x || !y || !fqh::aligned(x, elem(dtype)) || !fqh::aligned(y, elem(dtype))) return FQ_E_INVALID;
+    const size_t need = fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
+    if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    return dtype == FQ_F32 ? matmul<float>(x, m, n, k, group, *w, y, stream)
+                           : matmul<uint16_t>(x, m, n, k, group, *w, y, stream);
+}
+
+int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4* gate,
+                 const fql_w4* up, void* h, void* g, void* u, void* workspace, size_t workspace_bytes,
+                 hipStream_t stream) {
+    if (!fqh::valid_dtype(dtype) || (act != FQL_SILU && act != FQL_GELU)) return FQ_E_UNSUPPORTED;
+    if (!valid_sizes(m, n, k, group) || !valid_weight(gate) || !valid_weight(up)) return FQ_E_INVALID;
+    if (m == 0) return FQ_OK;
+    if (!x || !h || !g != !u) return FQ_E_INVALID;
+    for (const void* p : {x, (const void*)h, (const void*)g, (const void*)u})
+        if (!fqh::aligned(p, elem(dtype))) return FQ_E_INVALID;
+    const size_t need = fql_w4_gated_workspace_bytes(dtype, m, n, k, group);
+    if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    return dtype == FQ_F32 ? gated<float>(x, m, n, k, group, act, *gate, *up, h, g, u, stream)
+                           : gated<uint16_t>(x, m, n, k, group, act, *gate, *up, h, g, u, stream);
+}
+
+int fql_w4_matmul_backward(const void* dy, const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group,
+                           const fql_w4* w, void* dx, void* dw, int dw_dtype, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+    if (dtype != FQ_BF16 || !fqh::valid_dtype(dw_dtype)) return FQ_E_UNSUPPORTED;
+    if (!valid_sizes(m, n, k, group) || (!dx && !dw) || (dx && !valid_weight(w))) return FQ_E_INVALID;
+    if (!fqh::aligned(dx, 2) || !fqh::aligned(dw, elem(dw_dtype))) return FQ_E_INVALID;
+    if (m == 0) {
+        if (dw) fill_zero(dw, n * k * (int64_t)elem(dw_dtype), stream);
+        return fqh::launched();
+    }
+    if (!dy || !fqh::aligned(dy, 2) || (dw && (!x || !fqh::aligned(x, 2)))) return FQ_E_INVALID;
+    const size_t need = fql_w4_matmul_backward_workspace_bytes(m, n, k, group);
+    if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    if (dx) {
+        const W4Mat wm = w4_mat(*w, k, group);
+        const int st = run_tile(Dense<uint16_t>{(const uint16_t*)dy, n, 1}, W4Cols{wm, wm, n},
+                                Store<uint16_t>{(uint16_t*)dx, nullptr, k, m}, m, k, n, stream);
+        if (st != FQ_OK) return st;
+    }
+    return dw ? grad_weight(Dense<uint16_t>{(const uint16_t*)dy, 1, n}, x, m, n, n, k, dw, nullptr, dw_dtype, stream)
+              : FQ_OK;
+}
+
+int fql_w4_gated_backward(const void* dh, const void* x, const void* g, const void* u, int dtype, int64_t m, int64_t n,
+                          int64_t k, int64_t group, int act, const fql_w4* gate, const fql_w4* up, void* dx,
+                          void* dw_gate, void* dw_up, int dw_dtype, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+    if (dtype != FQ_BF16 || !fqh::valid_dtype(dw_dtype) || (act != FQL_SILU && act != FQL_GELU))
+        return FQ_E_UNSUPPORTED;
+    if (!valid_sizes(m, n, k, group) || !dw_gate != !dw_up || (!dx && !dw_gate)) return FQ_E_INVALID;
+    if (dx && (!valid_weight(gate) || !valid_weight(up))) return FQ_E_INVALID;
+    if (!fqh::aligned(dx, 2) || !fqh::aligned(dw_gate, elem(dw_dtype)) || !fqh::aligned(dw_up, elem(dw_dtype)))
+        return FQ_E_INVALID;
+    if (m == 0) {
+        if (dw_gate) {
+            fill_zero(dw_gate, n * k * (int64_t)elem(dw_dtype), stream);
+            fill_zero(dw_up, n * k * (int64_t)elem(dw_dtype), stream);
+        }
+        return fqh::launched();
+    }
+    if (!dh || !g || !u || (dw_gate && !x)) return FQ_E_INVALID;
+    for (const void* p : {dh, x, g, u})
+        if (!fqh::aligned(p, 2)) return FQ_E_INVALID;
+    const size_t need = fql_w4_gated_backward_workspace_bytes(m, n, k, group);
+    if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    GateGrad gr{(const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, n, act, false};
+    if (dx) {
+        const int st = run_tile(gr, W4Cols{w4_mat(*gate, k, group), w4_mat(*up, k, group), n},
+                                Store<uint16_t>{(uint16_t*)dx, nullptr, k, m}, m, k, 2 * n, stream);
+        if (st != FQ_OK) return st;
+    }
+    gr.tr = true;
+    return dw_gate ? grad_weight(gr, x, m, 2 * n, n, k, dw_gate, dw_up, dw_dtype, stream) : FQ_OK;
+}
+
+}  // extern "C"

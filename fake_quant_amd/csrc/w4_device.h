@@ -1,0 +1,65 @@
+// w4_device.h -- device-side pieces shared by the products with 4-bit
+// group-quantized weights (fq_linear.h): the stored matrix element by element,
+// bfloat16 conversion, the gated block's activations and their slopes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "fq_linear.h"
+
+namespace fqw {
+
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
+__device__ __forceinline__ float load_f(const float* p) { return *p; }
+__device__ __forceinline__ float load_f(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ __forceinline__ void store_f(float* p, float f) { *p = f; }
+__device__ __forceinline__ void store_f(uint16_t* p, float f) { *p = to_bf16(f); }
+
+// act(g) and act'(g).  silu: s = 1 / (1 + exp(-g)), g s and s (1 + g (1 - s)).
+// gelu: Phi(g) = erfc(-g / sqrt 2) / 2 (no cancellation in the lower tail), g Phi
+// and Phi + g phi(g), phi the standard normal density.
+__device__ __forceinline__ float act_value(int act, float g) {
+    if (act == FQL_SILU) return g / (1.0f + expf(-g));
+    return 0.5f * g * erfcf(-0.70710678118654752f * g);
+}
+__device__ __forceinline__ void act_both(int act, float g, float& value, float& slope) {
+    if (act == FQL_SILU) {
+        const float s = 1.0f / (1.0f + expf(-g));
+        value = g * s;
+        slope = s * fmaf(g, 1.0f - s, 1.0f);
+    } else {
+        const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+        value = g * p;
+        slope = fmaf(g * 0.39894228040143268f, expf(-0.5f * g * g), p);
+    }
+}
+
+// W[r, c] of one stored matrix (any group, any k).
+struct W4Mat {
+    const uint8_t* codes;
+    const float* scale;
+    const int32_t* zp;
+    int64_t k, group, row_bytes, ng;
+    __device__ __forceinline__ float at(int64_t r, int64_t c) const {
+        const uint32_t b = codes[r * row_bytes + (c >> 1)];
+        const int32_t q = (int32_t)(b << ((c & 1) ? 28 : 24)) >> 28;
+        const int64_t gi = r * ng + c / group;
+        return (float)(q - (zp ? zp[gi] : 0)) * scale[gi];
+    }
+};
+
+inline W4Mat w4_mat(const fql_w4& w, int64_t k, int64_t group) {
+    return W4Mat{w.codes, w.scale, w.zero_point, k, group, (k + 1) / 2, (k + group - 1) / group};
+}
+
+}  // namespace fqw

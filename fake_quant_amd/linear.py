@@ -1,0 +1,254 @@
+"""Products with 4-bit group-quantized weights (include/fq_linear.h): argument
+marshalling only, as in ``fake_quant_amd.fq``.
+
+Every function named ``fql_*`` calls the C entry point of the same name.  The
+helpers at the end (``w4_matmul`` ...) check shapes and types, allocate outputs
+and workspaces with torch, and call the ``fql_*`` functions on the current HIP
+stream.  A weight is the dict that ``fq.quant_groups(w, group, 4, scheme)``
+returns (``codes``, ``scale``, ``zp``; a missing or None ``zp`` stands for zeros,
+which is what symmetric weights hold).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import fq
+from .fq import (OK, BF16, E_DIM, E_INVALID, E_UNSUPPORTED, F32, FqError, _check, _I64, _INT, _lib, _need, _P, _ptr,
+                 _stream, _SZ)
+
+SILU, GELU = 0, 1
+ACTS = {"silu": SILU, "gelu": GELU}
+
+
+class W4(ctypes.Structure):
+    """fql_w4 (include/fq_linear.h): device addresses of one weight matrix."""
+    _fields_ = [("codes", _P), ("scale", _P), ("zero_point", _P)]
+
+
+_SIGS = {
+    "fql_w4_matmul_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _I64]),
+    "fql_w4_gated_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _I64]),
+    "fql_w4_matmul_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "fql_w4_gated_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "fql_w4_matmul": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "fql_w4_gated": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fql_w4_matmul_backward": (_INT, [_P, _P, _INT, _I64, _I64, _I64, _I64, _P, _P, _P, _INT, _P, _SZ, _P]),
+    "fql_w4_gated_backward": (_INT, [_P, _P, _P, _P, _INT, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _INT, _P,
+                                     _SZ, _P]),
+}
+for _name, (_res, _args) in _SIGS.items():
+    _fn = getattr(_lib, _name)
+    _fn.restype = _res
+    _fn.argtypes = _args
+
+EXPORTS = tuple(_SIGS)
+
+
+# ---------------------------------------------------------------------------
+# C entry points (same names, same argument order; tensors in, status checked).
+# A weight is given as a (codes, scale, zero_point or None) triple.
+# ---------------------------------------------------------------------------
+
+def _weight(nm, what, w, n, k, group):
+    codes, scale, zp = w
+    ng = -(-k // group) if group > 0 else 0
+    _need(nm, what + " codes", codes, n * ((k + 1) // 2))
+    _need(nm, what + " scale", scale, 4 * n * ng)
+    _need(nm, what + " zero_point", zp, 4 * n * ng)
+    return W4(_ptr(codes), _ptr(scale), _ptr(zp))
+
+
+def _ref(w):
+    return None if w is None else ctypes.byref(w)
+
+
+def fql_w4_matmul_workspace_bytes(dtype, m, n, k, group) -> int:
+    return _lib.fql_w4_matmul_workspace_bytes(dtype, m, n, k, group)
+
+
+def fql_w4_gated_workspace_bytes(dtype, m, n, k, group) -> int:
+    return _lib.fql_w4_gated_workspace_bytes(dtype, m, n, k, group)
+
+
+def fql_w4_matmul_backward_workspace_bytes(m, n, k, group) -> int:
+    return _lib.fql_w4_matmul_backward_workspace_bytes(m, n, k, group)
+
+
+def fql_w4_gated_backward_workspace_bytes(m, n, k, group) -> int:
+    return _lib.fql_w4_gated_backward_workspace_bytes(m, n, k, group)
+
+
+def fql_w4_matmul(x, dtype, m, n, k, group, w, y, workspace=None, workspace_bytes=0, stream=None):
+    nm = "fql_w4_matmul"
+    esz = 4 if dtype == F32 else 2
+    _need(nm, "x", x, esz * m * k)
+    _need(nm, "y", y, esz * m * n)
+    _need(nm, "workspace", workspace, workspace_bytes)
+    ws = _weight(nm, "w", w, n, k, group)
+    _check(nm, _lib.fql_w4_matmul(_ptr(x), dtype, m, n, k, group, _ref(ws), _ptr(y), _ptr(workspace), workspace_bytes,
+                                  _stream(stream)))
+
+
+def fql_w4_gated(x, dtype, m, n, k, group, act, gate, up, h, g=None, u=None, workspace=None, workspace_bytes=0,
+                 stream=None):
+    nm = "fql_w4_gated"
+    esz = 4 if dtype == F32 else 2
+    _need(nm, "x", x, esz * m * k)
+    for what, t in (("h", h), ("g", g), ("u", u)):
+        _need(nm, what, t, esz * m * n)
+    _need(nm, "workspace", workspace, workspace_bytes)
+    wg, wu = _weight(nm, "gate", gate, n, k, group), _weight(nm, "up", up, n, k, group)
+    _check(nm, _lib.fql_w4_gated(_ptr(x), dtype, m, n, k, group, act, _ref(wg), _ref(wu), _ptr(h), _ptr(g), _ptr(u),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fql_w4_matmul_backward(dy, x, dtype, m, n, k, group, w, dx, dw, dw_dtype, workspace=None, workspace_bytes=0,
+                           stream=None):
+    nm = "fql_w4_matmul_backward"
+    _need(nm, "dy", dy, 2 * m * n)
+    _need(nm, "x", x, 2 * m * k)
+    _need(nm, "dx", dx, 2 * m * k)
+    _need(nm, "dw", dw, (4 if dw_dtype == F32 else 2) * n * k)
+    _need(nm, "workspace", workspace, workspace_bytes)
+    ws = None if w is None else _weight(nm, "w", w, n, k, group)
+    _check(nm, _lib.fql_w4_matmul_backward(_ptr(dy), _ptr(x), dtype, m, n, k, group, _ref(ws), _ptr(dx), _ptr(dw),
+                                           dw_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def fql_w4_gated_backward(dh, x, g, u, dtype, m, n, k, group, act, gate, up, dx, dw_gate, dw_up, dw_dtype,
+                          workspace=None, workspace_bytes=0, stream=None):
+    nm = "fql_w4_gated_backward"
+    for what, t in (("dh", dh), ("g", g), ("u", u)):
+        _need(nm, what, t, 2 * m * n)
+    _need(nm, "x", x, 2 * m * k)
+    _need(nm, "dx", dx, 2 * m * k)
+    for what, t in (("dw_gate", dw_gate), ("dw_up", dw_up)):
+        _need(nm, what, t, (4 if dw_dtype == F32 else 2) * n * k)
+    _need(nm, "workspace", workspace, workspace_bytes)
+    wg = None if gate is None else _weight(nm, "gate", gate, n, k, group)
+    wu = None if up is None else _weight(nm, "up", up, n, k, group)
+    _check(nm, _lib.fql_w4_gated_backward(_ptr(dh), _ptr(x), _ptr(g), _ptr(u), dtype, m, n, k, group, act, _ref(wg),
+                                          _ref(wu), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), dw_dtype, _ptr(workspace),
+                                          workspace_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# helpers: shapes from the tensors, outputs and workspaces from torch
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _matrix(nm, what, t, rows=None, cols=None, dtype=None):
+    if t.dim() != 2:
+        raise FqError(nm, E_INVALID, f"{what} has {t.dim()} dimensions, not 2")
+    if t.dtype not in _DTYPES:
+        raise FqError(nm, E_UNSUPPORTED, f"{what} is {t.dtype}, neither float32 nor bfloat16")
+    if dtype is not None and t.dtype != dtype:
+        raise FqError(nm, E_DIM, f"{what} is {t.dtype}, not {dtype}")
+    if rows is not None and tuple(t.shape) != (rows, cols):
+        raise FqError(nm, E_DIM, f"{what} is {tuple(t.shape)}, not {(rows, cols)}")
+
+
+def _triple(nm, what, w, k, group, like):
+    """(codes, scale, zero_point) of a weight dict for rows of k columns, checked."""
+    if group < 1:
+        raise FqError(nm, E_INVALID, f"groups of {group}")
+    codes, scale, zp = w["codes"], w["scale"], w.get("zp")
+    if codes.dtype not in (torch.uint8, torch.int8) or scale.dtype != torch.float32 or \
+            (zp is not None and zp.dtype != torch.int32):
+        raise FqError(nm, E_UNSUPPORTED, f"{what} needs uint8 codes, float32 scale and int32 zp")
+    n = codes.shape[0]
+    if codes.dim() != 2 or codes.shape[1] != (k + 1) // 2:
+        raise FqError(nm, E_DIM, f"{what} codes are {tuple(codes.shape)}, not 4-bit rows of {k} columns")
+    want = (n, -(-k // group))
+    for part, t in (("scale", scale), ("zp", zp)):
+        if t is not None and tuple(t.shape) != want:
+            raise FqError(nm, E_DIM, f"{what} {part} is {tuple(t.shape)}, not {want}")
+    for part, t in (("codes", codes), ("scale", scale), ("zp", zp)):
+        if t is not None and t.device != like.device:
+            raise FqError(nm, E_INVALID, f"{what} {part} is on {t.device}, not {like.device}")
+    return (codes, scale, zp), n
+
+
+def _pair(nm, gate, up, k, group, like):
+    wg, n = _triple(nm, "gate", gate, k, group, like)
+    wu, n2 = _triple(nm, "up", up, k, group, like)
+    if n2 != n:
+        raise FqError(nm, E_DIM, f"gate has {n} rows, up {n2}")
+    return wg, wu, n
+
+
+def _act(nm, act):
+    if act not in ACTS:
+        raise FqError(nm, E_UNSUPPORTED, f"activation {act!r}, not one of {sorted(ACTS)}")
+    return ACTS[act]
+
+
+def _scratch(nbytes, like):
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
+def w4_matmul(x, w, group):
+    """x [m, k] (float32 or bfloat16) times the transpose of the [n, k] weight -> [m, n]."""
+    nm = "w4_matmul"
+    _matrix(nm, "x", x)
+    m, k = x.shape
+    w3, n = _triple(nm, "w", w, k, group, x)
+    dt = _DTYPES[x.dtype]
+    wsb = fql_w4_matmul_workspace_bytes(dt, m, n, k, group)
+    y = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    fql_w4_matmul(x, dt, m, n, k, group, w3, y, _scratch(wsb, x), wsb)
+    return y
+
+
+def w4_gated(x, gate, up, group, act="silu", save=False):
+    """act(x gate^T) * (x up^T) -> h, or (h, g, u) with save=True (what the backward pass reads)."""
+    nm = "w4_gated"
+    _matrix(nm, "x", x)
+    m, k = x.shape
+    wg, wu, n = _pair(nm, gate, up, k, group, x)
+    a, dt = _act(nm, act), _DTYPES[x.dtype]
+    wsb = fql_w4_gated_workspace_bytes(dt, m, n, k, group)
+    h = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
+    fql_w4_gated(x, dt, m, n, k, group, a, wg, wu, h, g, u, _scratch(wsb, x), wsb)
+    return (h, g, u) if save else h
+
+
+def w4_matmul_backward(dy, x, w, group, want_dx=True, want_dw=True, dw_dtype=torch.float32):
+    """(dx, dw) of y = x w^T for bfloat16 dy and x; dw is the straight-through gradient, None where not wanted."""
+    nm = "w4_matmul_backward"
+    _matrix(nm, "x", x)
+    m, k = x.shape
+    w3, n = _triple(nm, "w", w, k, group, x)
+    _matrix(nm, "dy", dy, m, n, x.dtype)
+    if dw_dtype not in _DTYPES:
+        raise FqError(nm, E_UNSUPPORTED, f"dw_dtype {dw_dtype}, neither float32 nor bfloat16")
+    wsb = fql_w4_matmul_backward_workspace_bytes(m, n, k, group)
+    dx = torch.empty_like(x) if want_dx else None
+    dw = torch.empty((n, k), dtype=dw_dtype, device=x.device) if want_dw else None
+    fql_w4_matmul_backward(dy, x, _DTYPES[x.dtype], m, n, k, group, w3, dx, dw, _DTYPES[dw_dtype], _scratch(wsb, x), wsb)
+    return dx, dw
+
+
+def w4_gated_backward(dh, x, g, u, gate, up, group, act="silu", want_dx=True, want_dw=True, dw_dtype=torch.bfloat16):
+    """(dx, dw_gate, dw_up) of h = act(x gate^T) * (x up^T) from dh and the forward pass's x, g and u."""
+    nm = "w4_gated_backward"
+    _matrix(nm, "x", x)
+    m, k = x.shape
+    wg, wu, n = _pair(nm, gate, up, k, group, x)
+    for what, t in (("dh", dh), ("g", g), ("u", u)):
+        _matrix(nm, what, t, m, n, x.dtype)
+    a = _act(nm, act)
+    if dw_dtype not in _DTYPES:
+        raise FqError(nm, E_UNSUPPORTED, f"dw_dtype {dw_dtype}, neither float32 nor bfloat16")
+    wsb = fql_w4_gated_backward_workspace_bytes(m, n, k, group)
+    dx = torch.empty_like(x) if want_dx else None
+    dwg, dwu = ((torch.empty((n, k), dtype=dw_dtype, device=x.device) for _ in range(2)) if want_dw
+                else (None, None))
+    fql_w4_gated_backward(dh, x, g, u, _DTYPES[x.dtype], m, n, k, group, a, wg, wu, dx, dwg, dwu, _DTYPES[dw_dtype],
+                          _scratch(wsb, x), wsb)
+    return dx, dwg, dwu

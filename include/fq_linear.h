@@ -1,0 +1,97 @@
+/*
+ * fq_linear.h -- C ABI of libfq.so: products with 4-bit group-quantized weights
+ * on AMD Instinct MI355X (gfx950), their gradients, and the gated feed-forward
+ * block built from them.
+ *
+ * The weights are what fq_quant_groups (fq.h) stores with bits = 4 for a
+ * row-major [n, k] matrix: codes packed two to a byte, ceil(k/2) bytes per row
+ * (even column in the high nibble, an odd row tail leaves the low nibble 0), and
+ * a float32 scale and int32 zero-point per group of `group` consecutive columns
+ * of a row, [n, ceil(k / group)].  The matrix they stand for is
+ *     W[r, c] = (code[r, c] - zero_point[r, c / group]) * scale[r, c / group],
+ * the values that fq_quant_groups writes as fake-quant values.
+ *
+ * Conventions are those of fq.h: device pointers owned by the caller, dense
+ * row-major layouts, nothing allocated and nothing synchronised, argument errors
+ * returned before anything is enqueued (FQ_E_INVALID, FQ_E_UNSUPPORTED, FQ_E_HIP),
+ * outputs that overlap neither inputs nor each other nor the workspace.  They
+ * differ in one point: m = 0 (no tokens) is a valid call, which writes no output
+ * with m rows and zeros to the gradients of the weights.
+ *
+ * Alignment: x, y, h, g, u, dy, dh, dx to their element size, scale and
+ * zero_point to 4 bytes, codes to any; the workspace to 16 bytes.
+ *
+ * Numbers: sums are held in binary32 and every output is rounded once to its
+ * type, ties to even.  Products of x with the integers code - zero_point are exact
+ * (a float32 x is split into three bfloat16 parts that sum to it), the scale
+ * multiplies each group's sum.  Inf and NaN in x, dy, dh, g or u give the Inf and
+ * NaN that the formulas give in the outputs whose sums hold them.  A backward pass
+ * rounds its factors; each entry point says how.  Two calls on the same arguments
+ * give the same bits.
+ */
+#ifndef FQ_LINEAR_H
+#define FQ_LINEAR_H
+
+#include "fq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* One group-quantized weight matrix (a HOST struct of device pointers).
+ * zero_point may be NULL: all zero, as FQ_SYM leaves them (4 bytes less to read
+ * per group).  Otherwise its values are those fq_quant_groups writes, -8 .. 7. */
+typedef struct {
+    const uint8_t* codes;
+    const float* scale;
+    const int32_t* zero_point;
+} fql_w4;
+
+/* Activations of the gated block: silu(g) = g / (1 + exp(-g)),
+ * gelu(g) = g Phi(g) with Phi the standard normal distribution (the erf form). */
+enum { FQL_SILU = 0, FQL_GELU = 1 };
+
+/* Workspace bytes of the calls below (0: none needed, workspace may be NULL).
+ * Host-only; 0 for arguments that the call refuses. */
+size_t fql_w4_matmul_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group);
+size_t fql_w4_gated_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group);
+size_t fql_w4_matmul_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t group);
+size_t fql_w4_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t group);
+
+/* y = x W^T: x [m, k] and y [m, n] of type dtype (FQ_F32 or FQ_BF16). */
+int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4* w, void* y,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The gated block's first half: h = act(x Wg^T) * (x Wu^T), both weights [n, k].
+ * h [m, n]; g = x Wg^T and u = x Wu^T [m, n] may be NULL (both or neither): what
+ * fql_w4_gated_backward reads.  All of type dtype.  h is formed from the binary32
+ * sums, not from the rounded g and u. */
+int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4* gate,
+                 const fql_w4* up, void* h, void* g, void* u, void* workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+
+/* Gradients of y = x W^T: dx = dy W (bfloat16 [m, k]) and dw = dy^T x ([n, k] of
+ * type dw_dtype, FQ_F32 or FQ_BF16), the latter the straight-through gradient of
+ * the weights that were quantized (min / max calibration leaves none outside its
+ * window).  dy [m, n] and x [m, k] bfloat16 (dtype other than FQ_BF16:
+ * FQ_E_UNSUPPORTED).  dx or dw may be NULL, not both; x may be NULL without dw, w
+ * without dx. */
+int fql_w4_matmul_backward(const void* dy, const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group,
+                           const fql_w4* w, void* dx, void* dw, int dw_dtype, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* Gradients of the gated block's first half from dh [m, n], its x, and the g and u
+ * that it wrote:
+ *   dg = dh u act'(g), du = dh act(g);  dx = dg Wg + du Wu (bfloat16 [m, k]),
+ *   dw_gate = dg^T x, dw_up = du^T x ([n, k] of type dw_dtype).
+ * Inputs bfloat16 (dtype as above).  dx, or the two dw together, may be NULL. */
+int fql_w4_gated_backward(const void* dh, const void* x, const void* g, const void* u, int dtype, int64_t m, int64_t n,
+                          int64_t k, int64_t group, int act, const fql_w4* gate, const fql_w4* up, void* dx,
+                          void* dw_gate, void* dw_up, int dw_dtype, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FQ_LINEAR_H */
