@@ -6,7 +6,8 @@
 // LDS, 16 sums per thread.  A and B are any functions of two indices (a dense
 // matrix, its transpose, a stored 4-bit matrix, a gradient formed from dh, g, u).
 #include "fq_host.h"
-#include "w4_device.h"
+#include "w4_linear.h"
+#include "w4_mfma.h"
 
 using namespace fqw;
 
@@ -178,6 +179,7 @@ int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int
     if (!x || !y || !fqh::aligned(x, elem(dtype)) || !fqh::aligned(y, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    if (m <= kFewTokens && span_of(group, k)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
     return dtype == FQ_F32 ? matmul<float>(x, m, n, k, group, *w, y, stream)
                            : matmul<uint16_t>(x, m, n, k, group, *w, y, stream);
 }
@@ -193,6 +195,8 @@ int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int6
         if (!fqh::aligned(p, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_gated_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    if (m <= kFewTokens && span_of(group, k))
+        return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
     return dtype == FQ_F32 ? gated<float>(x, m, n, k, group, act, *gate, *up, h, g, u, stream)
                            : gated<uint16_t>(x, m, n, k, group, act, *gate, *up, h, g, u, stream);
 }

@@ -1,0 +1,148 @@
+// w4_mfma.h -- how the matrix-instruction kernels read stored 4-bit weights and
+// token rows.
+//
+// One step of a kernel is 128 columns of W for 16 of its rows: lane l of a wave
+// holds 16 bytes (32 codes) of row l % 16, columns 32 (l / 16) .. + 31 of the step.
+// v_mfma_f32_16x16x32_bf16 takes 8 consecutive summation indices per lane, so a
+// lane's four dwords feed four instructions, and any assignment of the step's
+// columns to (instruction, lane) works as long as the token side follows it:
+//   Span 128: dword j of lane quarter q is columns 32 q + 8 j .. + 7;
+//   Span 64 / 32: the dwords are transposed between the lane quarters first (two
+//   permlane32 and two permlane16 swaps), so instruction j covers the 32
+//   consecutive columns 32 j .. + 31 and a group sum can end after one (32) or two
+//   (64) instructions.
+// Codes become bfloat16 through v_cvt_off_f32_i4, which gives code / 16 exactly;
+// the difference code - zero_point is an integer of at most 15 in magnitude, exact
+// in bfloat16.  Products with a bfloat16 x are exact in binary32, and the group's
+// scale (times 16) multiplies the group's sum: nothing is rounded but the sums.
+#pragma once
+
+#include "w4_device.h"
+
+namespace fqw {
+
+constexpr int kStep = 128;  // columns per step
+
+struct __attribute__((packed)) U32x4Any { u32x4 v; };
+__device__ __forceinline__ u32x4 load16(const void* p) { return reinterpret_cast<const U32x4Any*>(p)->v; }
+
+// (low nibble of byte B, sign-extended) / 16
+template <int B>
+__device__ __forceinline__ float cvt_i4(uint32_t w) {
+    float r;
+    if constexpr (B == 0)
+        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(r) : "v"(w));
+    else if constexpr (B == 1)
+        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(r) : "v"(w));
+    else if constexpr (B == 2)
+        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(r) : "v"(w));
+    else
+        asm("v_cvt_off_f32_i4_sdwa %0, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(r) : "v"(w));
+    return r;
+}
+
+// upper halves of two floats as a pair (first in the low half)
+__device__ __forceinline__ uint32_t pack_hi(float first, float second) {
+    return __builtin_amdgcn_perm(__float_as_uint(second), __float_as_uint(first), 0x07060302u);
+}
+
+template <bool ZP, int B>
+__device__ __forceinline__ uint32_t codes_pair(uint32_t w, uint32_t hi, float z16) {
+    float e = cvt_i4<B>(hi), o = cvt_i4<B>(w);  // even column in the high nibble
+    if constexpr (ZP) e -= z16, o -= z16;
+    return pack_hi(e, o);
+}
+
+// The eight codes of a dword as bfloat16 (code - zero_point) / 16; z16 = zero_point / 16.
+template <bool ZP>
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, float z16) {
+    const uint32_t hi = w >> 4;
+    const u32x4 r = {codes_pair<ZP, 0>(w, hi, z16), codes_pair<ZP, 1>(w, hi, z16), codes_pair<ZP, 2>(w, hi, z16),
+                     codes_pair<ZP, 3>(w, hi, z16)};
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// 4 x 4 transpose of dwords between the four lane quarters: afterwards dword j of
+// quarter q is what dword q of quarter j was.
+__device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+// Eight token values as matrix operands: bfloat16 as they are; float32 as three
+// bfloat16 parts that sum to x exactly (each part takes the next 8 significant
+// bits by truncation, so no part overflows).  Inf and NaN stay in the first part.
+template <class T>
+struct TokenFrag;
+template <>
+struct TokenFrag<uint16_t> {
+    static constexpr int kParts = 1;
+    bf16x8 p[1];
+    __device__ __forceinline__ void load(const uint16_t* s) { p[0] = __builtin_bit_cast(bf16x8, load16(s)); }
+    __device__ __forceinline__ void load_part(const uint16_t* s, int n) {  // the first n of 8, zeros after
+        uint32_t r[4] = {};
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r[i / 2] |= (uint32_t)s[i] << (16 * (i & 1));
+        p[0] = __builtin_bit_cast(bf16x8, u32x4{r[0], r[1], r[2], r[3]});
+    }
+};
+template <>
+struct TokenFrag<float> {
+    static constexpr int kParts = 3;
+    bf16x8 p[3];
+    __device__ __forceinline__ void split(const float (&f)[8]) {
+        uint32_t a[4], b[4], c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float r[2], s[2], h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                h[j] = __builtin_canonicalizef(f[2 * i + j]);  // a NaN keeps a bit in its upper half
+                const float top = __uint_as_float(__float_as_uint(h[j]) & 0xFFFF0000u);
+                r[j] = fabsf(h[j]) < INFINITY ? h[j] - top : 0.0f;
+                s[j] = r[j] - __uint_as_float(__float_as_uint(r[j]) & 0xFFFF0000u);
+            }
+            a[i] = pack_hi(h[0], h[1]);
+            b[i] = pack_hi(r[0], r[1]);
+            c[i] = pack_hi(s[0], s[1]);
+        }
+        p[0] = __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], a[2], a[3]});
+        p[1] = __builtin_bit_cast(bf16x8, u32x4{b[0], b[1], b[2], b[3]});
+        p[2] = __builtin_bit_cast(bf16x8, u32x4{c[0], c[1], c[2], c[3]});
+    }
+    __device__ __forceinline__ void load(const float* s) {
+        const u32x4 u = load16(s), v = load16(s + 4);
+        const float f[8] = {__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3]),
+                            __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
+        split(f);
+    }
+    __device__ __forceinline__ void load_part(const float* s, int n) {
+        float f[8];
+        for (int i = 0; i < 8; ++i) f[i] = i < n ? s[i] : 0.0f;
+        split(f);
+    }
+};
+
+// 16 code bytes at p of which `left` (may be <= 0) belong to the row; zeros after.
+__device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t left) {
+    if (left >= 16) return load16(p);
+    uint32_t r[4] = {};
+    for (int i = 0; i < 16; ++i)
+        if (i < left) r[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+    return u32x4{r[0], r[1], r[2], r[3]};
+}
+
+// Host: columns per group sum of the kernels (128, 64 or 32; 0: the group size is
+// none that they take).  A group of at least the whole row never ends inside it.
+inline int span_of(int64_t group, int64_t k) {
+    if (group >= k || group % 128 == 0) return 128;
+    return group % 64 == 0 ? 64 : group % 32 == 0 ? 32 : 0;
+}
+inline uint32_t spans_per_group(int64_t group, int64_t k, int span) {
+    return (uint32_t)((group < k ? group : k + span - 1) / span);
+}
+
+}  // namespace fqw
