@@ -134,6 +134,13 @@ bool valid_sizes(int64_t m, int64_t n, int64_t k, int64_t group) {
 bool valid_weight(const fql_w4* w) {
     return w && w->codes && w->scale && fqh::aligned(w->scale, 4) && fqh::aligned(w->zero_point, 4);
 }
+// Whether the matrix-instruction kernels read the weight: groups that end between
+// spans, 16 bytes of codes at least, offsets inside a tile under 2^31.
+bool regular(int64_t n, int64_t k, int64_t group) {
+    return span_of(group, k) && n * ((k + 1) / 2) >= 16 && k < kTileWidth;
+}
+bool few_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m <= kFewTokens && regular(n, k, group); }
+bool many_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m > kFewTokens && regular(n, k, group); }
 uintptr_t elem(int dtype) { return dtype == FQ_F32 ? 4 : 2; }
 
 template <class T>
@@ -166,8 +173,13 @@ int grad_weight(const A& a, const void* x, int64_t m, int64_t rows, int64_t n, i
 
 extern "C" {
 
-size_t fql_w4_matmul_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
-size_t fql_w4_gated_workspace_bytes(int, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t fql_w4_matmul_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group) {
+    if (!fqh::valid_dtype(dtype) || !valid_sizes(m, n, k, group)) return 0;
+    return many_tokens(m, n, k, group) ? forward_workspace(dtype, m, k) : 0;
+}
+size_t fql_w4_gated_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group) {
+    return fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
+}
 size_t fql_w4_matmul_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
 size_t fql_w4_gated_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
@@ -179,7 +191,9 @@ int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int
     if (!x || !y || !fqh::aligned(x, elem(dtype)) || !fqh::aligned(y, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
-    if (m <= kFewTokens && span_of(group, k)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
+    if (few_tokens(m, n, k, group)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
+    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)))
+        return forward_matmul(x, dtype, m, n, k, group, *w, y, workspace, stream);
     return dtype == FQ_F32 ? matmul<float>(x, m, n, k, group, *w, y, stream)
                            : matmul<uint16_t>(x, m, n, k, group, *w, y, stream);
 }
@@ -195,8 +209,9 @@ int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int6
         if (!fqh::aligned(p, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_gated_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
-    if (m <= kFewTokens && span_of(group, k))
-        return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
+    if (few_tokens(m, n, k, group)) return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
+    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)))
+        return forward_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, workspace, stream);
     return dtype == FQ_F32 ? gated<float>(x, m, n, k, group, act, *gate, *up, h, g, u, stream)
                            : gated<uint16_t>(x, m, n, k, group, act, *gate, *up, h, g, u, stream);
 }

@@ -54,7 +54,7 @@ struct FewWave {
             const W4Mat& w = a.w[t / NT];
             const int64_t r = wrow(t), b = step * (kStep / 2) + q * 16;
             const uint8_t* p = w.codes + r * w.row_bytes + b;
-            d.c[t] = whole ? load16(p) : load16_part(p, w.row_bytes - b);
+            d.c[t] = whole ? load16(p) : load16_part(p, (a.n - r) * w.row_bytes - b);  // codes past the row's end meet zeros
 #pragma unroll
             for (int i = 0; i < kSums; ++i) {
                 const int64_t g = r * w.ng + group_of((uint32_t)step * kSums + i);

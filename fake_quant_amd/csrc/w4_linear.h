@@ -13,4 +13,15 @@ int few_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_
 int few_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4& gate,
               const fql_w4& up, void* h, void* g, void* u, hipStream_t stream);
 
+// Widths under this keep 256 rows of three bfloat16 parts under 2^31 bytes.
+constexpr int64_t kTileWidth = (int64_t)1 << 20;
+
+// Any more rows of x.  x 16-byte aligned unless forward_workspace is not 0: the
+// workspace holds x in the layout that the tiles read, where x itself has another.
+size_t forward_workspace(int dtype, int64_t m, int64_t k);
+int forward_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4& w, void* y,
+                   void* workspace, hipStream_t stream);
+int forward_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4& gate,
+                  const fql_w4& up, void* h, void* g, void* u, void* workspace, hipStream_t stream);
+
 }  // namespace fqw

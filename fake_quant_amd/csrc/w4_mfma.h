@@ -126,13 +126,17 @@ struct TokenFrag<float> {
     }
 };
 
-// 16 code bytes at p of which `left` (may be <= 0) belong to the row; zeros after.
+// 16 code bytes at p of which `left` (may be <= 0) belong to the weight, whose 16
+// bytes or more end there: read from its end and moved down, zeros after.
 __device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t left) {
     if (left >= 16) return load16(p);
-    uint32_t r[4] = {};
-    for (int i = 0; i < 16; ++i)
-        if (i < left) r[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
-    return u32x4{r[0], r[1], r[2], r[3]};
+    if (left <= 0) return u32x4{0, 0, 0, 0};
+    const u32x4 v = load16(p + left - 16);
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    int bits = 8 * (16 - (int)left);  // 8 .. 120
+    if (bits >= 64) lo = hi, hi = 0, bits -= 64;
+    if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // Host: columns per group sum of the kernels (128, 64 or 32; 0: the group size is
