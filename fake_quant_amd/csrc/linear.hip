@@ -141,6 +141,11 @@ bool regular(int64_t n, int64_t k, int64_t group) {
 }
 bool few_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m <= kFewTokens && regular(n, k, group); }
 bool many_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m > kFewTokens && regular(n, k, group); }
+bool tiled_backward(int64_t n, int64_t k, int64_t group) { return regular(n, k, group) && n < kTileWidth; }
+// Whether a matrix of rows of c elements of 2 bytes is read in place or copied first.
+bool chunked(const void* p, int64_t c) { return c % 8 || fqh::aligned(p, 16); }
+// Whether rows of c elements of e bytes may be stored in 16-byte pieces, or are not at all.
+bool stored_whole(const void* p, int64_t c, uintptr_t e) { return c % (16 / e) || fqh::aligned(p, 16); }
 uintptr_t elem(int dtype) { return dtype == FQ_F32 ? 4 : 2; }
 
 template <class T>
@@ -180,8 +185,12 @@ size_t fql_w4_matmul_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k,
 size_t fql_w4_gated_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group) {
     return fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
 }
-size_t fql_w4_matmul_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
-size_t fql_w4_gated_backward_workspace_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t fql_w4_matmul_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t group) {
+    return valid_sizes(m, n, k, group) && tiled_backward(n, k, group) ? backward_workspace(m, n, k, false) : 0;
+}
+size_t fql_w4_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t group) {
+    return valid_sizes(m, n, k, group) && tiled_backward(n, k, group) ? backward_workspace(m, n, k, true) : 0;
+}
 
 int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4* w, void* y,
                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
@@ -229,6 +238,9 @@ int fql_w4_matmul_backward(const void* dy, const void* x, int dtype, int64_t m, 
     if (!dy || !fqh::aligned(dy, 2) || (dw && (!x || !fqh::aligned(x, 2)))) return FQ_E_INVALID;
     const size_t need = fql_w4_matmul_backward_workspace_bytes(m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    if (tiled_backward(n, k, group) && chunked(dy, n) && (!dw || chunked(x, k)) && stored_whole(dx, k, 2) &&
+        stored_whole(dw, k, elem(dw_dtype)))
+        return matmul_backward(dy, x, m, n, k, group, w, dx, dw, dw_dtype, workspace, stream);
     if (dx) {
         const W4Mat wm = w4_mat(*w, k, group);
         const int st = run_tile(Dense<uint16_t>{(const uint16_t*)dy, n, 1}, W4Cols{wm, wm, n},
@@ -261,6 +273,10 @@ int fql_w4_gated_backward(const void* dh, const void* x, const void* g, const vo
         if (!fqh::aligned(p, 2)) return FQ_E_INVALID;
     const size_t need = fql_w4_gated_backward_workspace_bytes(m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
+    if (tiled_backward(n, k, group) && (!dw_gate || chunked(x, k)) && stored_whole(dx, k, 2) &&
+        stored_whole(dw_gate, k, elem(dw_dtype)) && stored_whole(dw_up, k, elem(dw_dtype)))
+        return gated_backward(dh, x, g, u, m, n, k, group, act, gate, up, dx, dw_gate, dw_up, dw_dtype, workspace,
+                              stream);
     GateGrad gr{(const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, n, act, false};
     if (dx) {
         const int st = run_tile(gr, W4Cols{w4_mat(*gate, k, group), w4_mat(*up, k, group), n},

@@ -58,10 +58,11 @@ __device__ __forceinline__ u32x4 buffer(const void* p, uint32_t bytes) {
 // 16 bytes a lane from offset `off` of a buffer to 1 KiB of LDS at dst (one address per
 // wave, in M0, which nothing else here uses).  Written out, because the compiler's own
 // form makes every later LDS read wait for it; wait_dma() ends such loads.  There is
-// no destination register that could be reused meanwhile.
+// no destination register that could be reused meanwhile.  The wait states cover a
+// descriptor or address that the vector unit has just put into scalar registers (5).
 __device__ __forceinline__ void dma16(u32x4 b, uint16_t* dst, uint32_t off) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(b)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(b)
                  : "memory");
 }
 __device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
