@@ -135,13 +135,14 @@ bool valid_weight(const fql_w4* w) {
     return w && w->codes && w->scale && fqh::aligned(w->scale, 4) && fqh::aligned(w->zero_point, 4);
 }
 // Whether the matrix-instruction kernels read the weight: groups that end between
-// spans, 16 bytes of codes at least, offsets inside a tile under 2^31.
+// spans, 16 bytes of codes and rows of 8 columns at least, offsets inside a tile
+// under 2^31.
 bool regular(int64_t n, int64_t k, int64_t group) {
-    return span_of(group, k) && n * ((k + 1) / 2) >= 16 && k < kTileWidth;
+    return span_of(group, k) && n * ((k + 1) / 2) >= 16 && k >= 8 && k < kTileWidth;
 }
 bool few_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m <= kFewTokens && regular(n, k, group); }
 bool many_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m > kFewTokens && regular(n, k, group); }
-bool tiled_backward(int64_t n, int64_t k, int64_t group) { return regular(n, k, group) && n < kTileWidth; }
+bool tiled_backward(int64_t n, int64_t k, int64_t group) { return regular(n, k, group) && n >= 8 && n < kTileWidth; }
 // Whether a matrix of rows of c elements of 2 bytes is read in place or copied first.
 bool chunked(const void* p, int64_t c) { return c % 8 || fqh::aligned(p, 16); }
 // Whether rows of c elements of e bytes may be stored in 16-byte pieces, or are not at all.

@@ -205,20 +205,16 @@ __global__ __launch_bounds__(256) void k_gate_grad(const uint16_t* dh, const uin
     const int64_t chunks = run / 8;
     for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < m * chunks; v += gridDim.x * 256ll) {
         const int64_t r = v / chunks, c = v % chunks * 8, at = r * n + c;
-        TokenFrag<uint16_t> d, gg, uu;
-        if (c + 8 <= n) {
-            d.load(dh + at), gg.load(g + at), uu.load(u + at);
-        } else {
-            const int left = (int)(n > c ? n - c < 8 ? n - c : 8 : 0);
-            d.load_part(dh + at, left), gg.load_part(g + at, left), uu.load_part(u + at, left);
-        }
-        bf16x8 dg, du;
+        Tokens<uint16_t> td, tg, tu;
+        td.load_part(dh + at, n - c), tg.load_part(g + at, n - c), tu.load_part(u + at, n - c);
+        bf16x8 d[1], gg[1], uu[1], dg, du;
+        td.parts(d), tg.parts(gg), tu.parts(uu);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float value, slope;
-            const float di = (float)d.p[0][i];
-            act_both(act, (float)gg.p[0][i], value, slope);
-            dg[i] = (__bf16)(di * (float)uu.p[0][i] * slope);
+            const float di = (float)d[0][i];
+            act_both(act, (float)gg[0][i], value, slope);
+            dg[i] = (__bf16)(di * (float)uu[0][i] * slope);
             du[i] = (__bf16)(di * value);
         }
         *reinterpret_cast<bf16x8*>(out + r * 2 * run + c) = dg;
@@ -232,10 +228,9 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t* in, int64_t ro
     const int64_t chunks = ld / 8;
     for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < rows * chunks; v += gridDim.x * 256ll) {
         const int64_t r = v / chunks, c = v % chunks * 8;
-        TokenFrag<uint16_t> f;
-        if (c + 8 <= cols) f.load(in + r * cols + c);
-        else f.load_part(in + r * cols + c, (int)(cols - c));
-        *reinterpret_cast<bf16x8*>(out + r * ld + c) = f.p[0];
+        Tokens<uint16_t> f;
+        f.load_part(in + r * cols + c, cols - c);
+        *reinterpret_cast<u32x4*>(out + r * ld + c) = f.v;
     }
 }
 

@@ -14,139 +14,243 @@ namespace fqw {
 namespace {
 
 constexpr int kFewWaves = 8;
-constexpr int kAhead = 4;  // steps whose codes a wave loads before it uses the first
 
 template <class T>
 struct FewArgs {
     const T* x;
     W4Mat w[2];
-    T *out[3];  // y, or h, g, u
+    T* out[3];  // y, or h, g, u
     int64_t m, n, k;
-    uint32_t spans, per_group;  // spans in a row, spans in a group
+    uint32_t spans, inverse;  // spans in a row; ceil(2^31 / spans in a group)
     int act;
+    // one weight of a pair may have no zero-points: then any readable words, masked to zeros
+    const int32_t* zp[2];
+    int32_t mask[2];
 };
 
-template <class T, int MT, int NT, int SPAN, bool ZP, int W>
+// What one wave does: M4 x 4 tokens (M4 = 1, or a multiple of 4) and NT x 16 rows of
+// each of W weights, AHEAD steps in flight.  Memory delivers 64 bytes a cycle where
+// four neighbouring lanes ask for 64 consecutive ones, and a quarter of that where
+// each lane of the four is in another row, as the matrix instruction's operands
+// are.  So a lane loads for the memory's sake (4 lanes a row of codes, 16 or 32 a
+// row of x) and the wave's own corner of LDS turns the data; DS operations of a
+// wave stay in order, no barrier is needed.
+template <class T, int M4, int NT, int SPAN, bool ZP, int W, int AHEAD>
 struct FewWave {
-    static constexpr int kTiles = NT * W, kSums = kStep / SPAN;
-    const FewArgs<T>& a;
-    int64_t n0;
-    int lane, row, q;
-    f32x4 acc[MT][kTiles];
+    static constexpr int MT = (M4 + 3) / 4, kTiles = NT * W, kSums = kStep / SPAN, kDots = SPAN / 32;
+    static constexpr int kParts = Tokens<T>::kParts, kHalves = sizeof(T) / 2;  // 16-byte loads per 4 rows of x
+    static constexpr int kChunks = 16 * kHalves;                               // 16-byte chunks in a row of x
+    static constexpr int kStats = (AHEAD * kSums + 3) / 4, kPitch = kStats * 4 + 1;
 
-    struct Codes {
-        u32x4 c[kTiles];
-        float s[kTiles][kSums], z[kTiles][kSums];
+    struct Lds {
+        u32x4 x[16 * kChunks];
+        u32x4 c[kTiles][64];
+        float s[kTiles][16 * kPitch], z[ZP ? kTiles : 1][ZP ? 16 * kPitch : 1];
+    };
+    struct Step {
+        u32x4 c[kTiles], x[M4 * kHalves];
+    };
+    struct Stats {  // of AHEAD steps
+        float s[kTiles][kStats];
+        int32_t z[kTiles][kStats];
     };
 
-    __device__ __forceinline__ int64_t wrow(int t) const {
+    const FewArgs<T>& a;
+    Lds& lds;
+    int64_t m0, n0;
+    int lane;
+    f32x4 acc[MT][kTiles];
+
+    __device__ __forceinline__ int64_t wrow(int t, int row) const {
         const int64_t r = n0 + 16 * (t % NT) + row;
         return r < a.n ? r : a.n - 1;
     }
-    // group of span number s of a row (a span past the row's end belongs to its last group)
-    __device__ __forceinline__ uint32_t group_of(uint32_t s) const {
-        s = s < a.spans ? s : a.spans - 1;
-        return a.per_group == 1 ? s : s / a.per_group;
-    }
-    __device__ __forceinline__ void fetch(Codes& d, int64_t step, bool whole) const {
+    // WHOLE: all of the step's columns exist.
+    template <bool WHOLE>
+    __device__ __forceinline__ void fetch(Step& d, uint32_t step) const {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             const W4Mat& w = a.w[t / NT];
-            const int64_t r = wrow(t), b = step * (kStep / 2) + q * 16;
+            const int64_t r = wrow(t, lane / 4), b = (int64_t)step * (kStep / 2) + lane % 4 * 16;
             const uint8_t* p = w.codes + r * w.row_bytes + b;
-            d.c[t] = whole ? load16(p) : load16_part(p, (a.n - r) * w.row_bytes - b);  // codes past the row's end meet zeros
+            // past the row's end a lane reads codes of the next row, which meet zeros of x
+            d.c[t] = WHOLE ? load16(p) : load16_part(p, (a.n - r) * w.row_bytes - b);
+        }
 #pragma unroll
-            for (int i = 0; i < kSums; ++i) {
-                const int64_t g = r * w.ng + group_of((uint32_t)step * kSums + i);
-                d.s[t][i] = w.scale[g] * 16.0f;
-                if constexpr (ZP) d.z[t][i] = w.zp ? (float)w.zp[g] * 0.0625f : 0.0f;
-                else d.z[t][i] = 0.0f;
+        for (int i = 0; i < M4 * kHalves; ++i) {
+            const int64_t at = m0 + i * (4 / kHalves) + lane / kChunks, r = at < a.m ? at : a.m - 1;
+            const int64_t c = (int64_t)step * kStep + lane % kChunks * (16 / sizeof(T));
+            const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x + r * a.k + c);
+            d.x[i] = WHOLE ? load16(p) : load16_part(p, (a.k - c) * (int64_t)sizeof(T));
+        }
+    }
+    // Scales and zero-points of the spans of AHEAD steps from `step` on.
+    __device__ __forceinline__ void fetch_stats(Stats& d, uint32_t step) const {
+#pragma unroll
+        for (int i = 0; i < kStats; ++i) {
+            uint32_t g = step * kSums + 4 * i + lane % 4;
+            g = g < a.spans ? g : a.spans - 1;  // a span past the row's end belongs to its last group
+            g = (uint32_t)((uint64_t)g * a.inverse >> 31);  // exact: spans and spans in a group are under 2^15
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int64_t at = wrow(t, lane / 4) * a.w[0].ng + g;
+                d.s[t][i] = a.w[t / NT].scale[at];
+                if constexpr (ZP) d.z[t][i] = a.zp[t / NT][at] & a.mask[t / NT];
             }
         }
     }
-    __device__ __forceinline__ void tokens(TokenFrag<T>& f, int mt, int j, int64_t step, bool whole) const {
-        const int64_t r = 16 * mt + row;
-        const T* p = a.x + (r < a.m ? r : a.m - 1) * a.k;
-        const int64_t c = step * kStep + (SPAN == 128 ? 32 * q + 8 * j : 32 * j + 8 * q);
-        if (whole) f.load(p + c);
-        else f.load_part(p + c, (int)(a.k - c < 8 ? a.k - c : 8));
+    __device__ __forceinline__ void turn() const {  // what other lanes wrote before is read after
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
-    __device__ __forceinline__ void use(const Codes& d, int64_t step, bool whole) {
-        u32x4 c[kTiles];
+    __device__ __forceinline__ void keep_stats(const Stats& d) {
+        turn();
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) c[t] = SPAN == 128 ? d.c[t] : transpose_quarters(d.c[t]);
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int i = 0; i < kSums; ++i) {
-            f32x4 part[MT][kTiles];
+            for (int i = 0; i < kStats; ++i) {
+                const int at = lane / 4 * kPitch + 4 * i + lane % 4;
+                lds.s[t][at] = d.s[t][i] * 16.0f;
+                if constexpr (ZP) lds.z[t][at] = (float)d.z[t][i] * 0.0625f;
+            }
+        turn();
+    }
+    __device__ __forceinline__ void keep_tokens(const Step& d, int mt) {
 #pragma unroll
-            for (int j = 0; j < SPAN / 32; ++j) {
-                bf16x8 b[kTiles];
+        for (int i = 0; i < (M4 < 4 ? M4 : 4) * kHalves; ++i) {
+            const int r = i * (4 / kHalves) + lane / kChunks;
+            lds.x[r * kChunks + (lane % kChunks ^ (r & 7))] = d.x[mt * 4 * kHalves + i];
+        }
+    }
+    // number: which of the AHEAD steps that the kept scales are for
+    __device__ __forceinline__ void use(const Step& d, int number) {
+        const int row = lane % 16, q = lane / 16;
+        turn();
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) b[t] = codes_bf16<ZP>(c[t][i * (SPAN / 32) + j], d.z[t][i]);
+        for (int t = 0; t < kTiles; ++t) lds.c[t][lane / 4 * 4 + (lane % 4 ^ (lane / 8 & 3))] = d.c[t];
+        keep_tokens(d, 0);
+        turn();
+        bf16x8 b[kTiles][4];
+        float s[kTiles][kSums];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    TokenFrag<T> f;
-                    tokens(f, mt, i * (SPAN / 32) + j, step, whole);
+        for (int t = 0; t < kTiles; ++t) {
+            u32x4 c = lds.c[t][row * 4 + (q ^ (row / 2 & 3))];
+            if (SPAN != 128) c = transpose_quarters(c);
 #pragma unroll
-                    for (int p = 0; p < TokenFrag<T>::kParts; ++p)
+            for (int i = 0; i < kSums; ++i) {
+                const int at = row * kPitch + number * kSums + i;
+                const float z = ZP ? lds.z[t][at] : 0.0f;
+                s[t][i] = lds.s[t][at];
 #pragma unroll
-                        for (int t = 0; t < kTiles; ++t)
-                            part[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                f.p[p], b[t], j || p ? part[mt][t] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+                for (int j = i * kDots; j < (i + 1) * kDots; ++j) b[t][j] = codes_bf16<ZP>(c[j], z);
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            bf16x8 f[4][kParts];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int chunk = (SPAN == 128 ? 4 * q + j : 4 * j + q) * kHalves;
+                Tokens<T> v;
+                if constexpr (kHalves == 1) {
+                    v.v = lds.x[row * kChunks + (chunk ^ (row & 7))];
+                } else {
+                    v.v[0] = lds.x[row * kChunks + (chunk ^ (row & 7))];
+                    v.v[1] = lds.x[row * kChunks + (chunk + 1 ^ (row & 7))];
                 }
+                v.parts(f[j]);
+            }
+            if (mt + 1 < MT) {
+                turn();
+                keep_tokens(d, mt + 1);
+                turn();
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int i = 0; i < kSums; ++i) {
+                f32x4 part[kTiles] = {};
+#pragma unroll
+                for (int j = i * kDots; j < (i + 1) * kDots; ++j)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+                            part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][p], b[t][j], part[t], 0, 0, 0);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[mt][t][e] = fmaf(part[mt][t][e], d.s[t][i], acc[mt][t][e]);
+                    for (int e = 0; e < 4; ++e) acc[mt][t][e] = fmaf(part[t][e], s[t][i], acc[mt][t][e]);
+            }
         }
     }
 };
 
 // W = 1: y = x W^T.  W = 2: w[0] is the gate, w[1] the up matrix.
-template <class T, int MT, int NT, int SPAN, bool ZP, int W>
-__global__ __launch_bounds__(64 * kFewWaves) void k_few(FewArgs<T> a) {
-    using Wave = FewWave<T, MT, NT, SPAN, ZP, W>;
-    constexpr int kTiles = Wave::kTiles;
-    __shared__ f32x4 sums[kFewWaves][MT * kTiles][64];
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    Wave v{a, (int64_t)blockIdx.x * 16 * NT, lane, lane % 16, lane / 16, {}};
-    const int64_t full = a.k / kStep;
-    for (int64_t s = wave; s < full; s += kFewWaves * kAhead) {
-        typename Wave::Codes d[kAhead];
+template <class T, int M4, int NT, int SPAN, bool ZP, int W, int AHEAD>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void k_few(FewArgs<T> a) {
+    using Wave = FewWave<T, M4, NT, SPAN, ZP, W, AHEAD>;
+    constexpr int MT = Wave::MT, kTiles = Wave::kTiles;
+    __shared__ union {
+        typename Wave::Lds own[kFewWaves];
+        f32x4 sums[kFewWaves][MT * kTiles][64];
+    } lds;
+    const int lane = threadIdx.x % 64;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    Wave v{a, lds.own[wave], (int64_t)blockIdx.y * 4 * M4, (int64_t)blockIdx.x * 16 * NT, lane, {}};
+    // each wave takes a run of the row's steps, the last one also the row's short step
+    const uint32_t full = (uint32_t)(a.k / kStep), run = (full + kFewWaves - 1) / kFewWaves;
+    uint32_t s = wave * run;
+    const uint32_t end = s + run < full ? s + run : full;
+    typename Wave::Stats st;
+    if (s < end) {
+        typename Wave::Step d[AHEAD];
+        // loads past the run repeat its last step, which keeps the loop free of branches
+        const auto next = [&](uint32_t i) { return i < end ? i : end - 1; };
+        v.fetch_stats(st, s);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (s + i * kFewWaves < full) v.fetch(d[i], s + i * kFewWaves, true);
+        for (int i = 0; i < AHEAD; ++i) v.template fetch<true>(d[i], next(s + i));
+        for (; s + AHEAD < end; s += AHEAD) {
+            v.keep_stats(st);
+            v.fetch_stats(st, s + AHEAD);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (s + i * kFewWaves < full) v.use(d[i], s + i * kFewWaves, true);
+            for (int i = 0; i < AHEAD; ++i) {
+                v.use(d[i], i);
+                v.template fetch<true>(d[i], next(s + AHEAD + i));
+            }
+        }
+        v.keep_stats(st);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (s + i < end) v.use(d[i], i);
     }
-    if (full * kStep < a.k && full % kFewWaves == wave) {  // the row's last, short step
-        typename Wave::Codes d;
-        v.fetch(d, full, false);
-        v.use(d, full, false);
+    if (full * (int64_t)kStep < a.k && wave == kFewWaves - 1) {
+        typename Wave::Step d;
+        v.fetch_stats(st, full);
+        v.template fetch<false>(d, full);
+        v.keep_stats(st);
+        v.use(d, 0);
     }
+    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) sums[wave][mt * kTiles + t][lane] = v.acc[mt][t];
+        for (int t = 0; t < kTiles; ++t) lds.sums[wave][mt * kTiles + t][lane] = v.acc[mt][t];
     __syncthreads();
     for (int o = wave; o < MT * NT; o += kFewWaves) {
         const int mt = o / NT, nt = o % NT;
-        const int64_t c = v.n0 + 16 * nt + v.row;
+        const int64_t c = v.n0 + 16 * nt + lane % 16;
         f32x4 r[W];
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            r[w] = sums[0][mt * kTiles + w * NT + nt][lane];
-            for (int i = 1; i < kFewWaves; ++i) r[w] += sums[i][mt * kTiles + w * NT + nt][lane];
+            r[w] = lds.sums[0][mt * kTiles + w * NT + nt][lane];
+#pragma unroll
+            for (int i = 1; i < kFewWaves; ++i) r[w] += lds.sums[i][mt * kTiles + w * NT + nt][lane];
         }
         if (c >= a.n) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t i = 16 * mt + 4 * v.q + e;
-            if (i >= a.m) continue;
+            const int in = 16 * mt + 4 * (lane / 16) + e;
+            const int64_t i = v.m0 + in;
+            if (in >= 4 * M4 || i >= a.m) continue;
             const int64_t at = i * a.n + c;
             if constexpr (W == 1) {
                 store_f(a.out[0] + at, r[0][e]);
@@ -161,45 +265,56 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(FewArgs<T> a) {
     }
 }
 
-template <class T, int MT, int NT, int W>
-int launch(const FewArgs<T>& a, int span, hipStream_t stream) {
-    const int64_t blocks = (a.n + 16 * NT - 1) / (16 * NT);
-    if (blocks > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
-    const bool zp = a.w[0].zp || (W == 2 && a.w[1].zp);
-    const dim3 g((unsigned)blocks), b(64 * kFewWaves);
-    if (span == 128) zp ? k_few<T, MT, NT, 128, true, W><<<g, b, 0, stream>>>(a) : k_few<T, MT, NT, 128, false, W><<<g, b, 0, stream>>>(a);
-    else if (span == 64) zp ? k_few<T, MT, NT, 64, true, W><<<g, b, 0, stream>>>(a) : k_few<T, MT, NT, 64, false, W><<<g, b, 0, stream>>>(a);
-    else zp ? k_few<T, MT, NT, 32, true, W><<<g, b, 0, stream>>>(a) : k_few<T, MT, NT, 32, false, W><<<g, b, 0, stream>>>(a);
+template <class T, int M4, int NT, bool ZP, int W, int AHEAD>
+void few_span(FewArgs<T> a, int64_t group, dim3 g, hipStream_t stream) {
+    constexpr int kThreads = 64 * kFewWaves;
+    const int span = span_of(group, a.k);
+    const uint32_t per = spans_per_group(group, a.k, span);
+    a.spans = (uint32_t)((a.k + span - 1) / span);
+    a.inverse = (uint32_t)((((uint64_t)1 << 31) + per - 1) / per);
+    for (int i = 0; i < 2; ++i) {
+        a.zp[i] = a.w[i].zp ? a.w[i].zp : reinterpret_cast<const int32_t*>(a.w[i].scale);
+        a.mask[i] = a.w[i].zp ? -1 : 0;
+    }
+    if (span == 128) k_few<T, M4, NT, 128, ZP, W, AHEAD><<<g, kThreads, 0, stream>>>(a);
+    else if (span == 64) k_few<T, M4, NT, 64, ZP, W, AHEAD><<<g, kThreads, 0, stream>>>(a);
+    else k_few<T, M4, NT, 32, ZP, W, AHEAD><<<g, kThreads, 0, stream>>>(a);
+}
+
+template <class T, int M4, int NT, int W, int AHEAD>
+int launch(const FewArgs<T>& a, int64_t group, hipStream_t stream) {
+    const int64_t x = (a.n + 16 * NT - 1) / (16 * NT), y = (a.m + 4 * M4 - 1) / (4 * M4);
+    if (x > 0x7FFFFFFF || y > 0xFFFF) return FQ_E_UNSUPPORTED;
+    const dim3 g((unsigned)x, (unsigned)y);
+    if (a.w[0].zp || a.w[1].zp) few_span<T, M4, NT, true, W, AHEAD>(a, group, g, stream);
+    else few_span<T, M4, NT, false, W, AHEAD>(a, group, g, stream);
     return fqh::launched();
 }
 
 template <class T, int W>
-int few(const FewArgs<T>& a, int span, hipStream_t stream) {
-    if (a.m <= 16) return launch<T, 1, 1, W>(a, span, stream);
-    if (a.m <= 32) return launch<T, 2, 1, W>(a, span, stream);
-    return launch<T, 4, 1, W>(a, span, stream);
+int few(const FewArgs<T>& a, int64_t group, hipStream_t stream) {
+    if (a.m <= 4) return launch<T, 1, 1, W, 4>(a, group, stream);
+    if constexpr (sizeof(T) == 4) return a.m <= 16 ? launch<T, 4, 1, W, 1>(a, group, stream) : launch<T, 8, 2 / W, W, 1>(a, group, stream);
+    if (a.m <= 16) return launch<T, 4, 1, W, 2>(a, group, stream);
+    return a.m <= 32 ? launch<T, 8, 2 / W, W, 1>(a, group, stream) : launch<T, 16, 2 / W, W, 1>(a, group, stream);
 }
 
 }  // namespace
 
 int few_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4& w, void* y,
                hipStream_t stream) {
-    const int span = span_of(group, k);
-    const uint32_t spans = (uint32_t)((k + span - 1) / span), per = spans_per_group(group, k, span);
     const W4Mat wm = w4_mat(w, k, group);
-    if (dtype == FQ_F32) return few<float, 1>({(const float*)x, {wm, wm}, {(float*)y}, m, n, k, spans, per, 0}, span, stream);
-    return few<uint16_t, 1>({(const uint16_t*)x, {wm, wm}, {(uint16_t*)y}, m, n, k, spans, per, 0}, span, stream);
+    if (dtype == FQ_F32) return few<float, 1>({(const float*)x, {wm, wm}, {(float*)y}, m, n, k}, group, stream);
+    return few<uint16_t, 1>({(const uint16_t*)x, {wm, wm}, {(uint16_t*)y}, m, n, k}, group, stream);
 }
 
 int few_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4& gate,
               const fql_w4& up, void* h, void* g, void* u, hipStream_t stream) {
-    const int span = span_of(group, k);
-    const uint32_t spans = (uint32_t)((k + span - 1) / span), per = spans_per_group(group, k, span);
     const W4Mat wg = w4_mat(gate, k, group), wu = w4_mat(up, k, group);
     if (dtype == FQ_F32)
-        return few<float, 2>({(const float*)x, {wg, wu}, {(float*)h, (float*)g, (float*)u}, m, n, k, spans, per, act}, span, stream);
-    return few<uint16_t, 2>({(const uint16_t*)x, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k, spans, per, act}, span,
-                            stream);
+        return few<float, 2>({(const float*)x, {wg, wu}, {(float*)h, (float*)g, (float*)u}, m, n, k, 0, 0, act}, group, stream);
+    return few<uint16_t, 2>({(const uint16_t*)x, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k, 0, 0, act},
+                            group, stream);
 }
 
 }  // namespace fqw

@@ -159,16 +159,17 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_forward(ForwardArgs<T> a) {
 // past the row's end.  float32 in three parts, bfloat16 as it is.
 template <class T>
 __global__ __launch_bounds__(256) void k_pieces(const T* x, int64_t m, int64_t k, int64_t kp, uint16_t* out) {
-    constexpr int P = TokenFrag<T>::kParts;
+    constexpr int P = Tokens<T>::kParts;
     const int64_t chunks = kp / 8;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m * chunks; i += gridDim.x * 256ll) {
         const int64_t r = i / chunks, c = i % chunks * 8;
-        TokenFrag<T> f;
-        if (c + 8 <= k) f.load(x + r * k + c);
-        else f.load_part(x + r * k + c, (int)(k > c ? k - c : 0));
+        Tokens<T> f;
+        f.load_part(x + r * k + c, k - c);
+        bf16x8 v[P];
+        f.parts(v);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            *reinterpret_cast<bf16x8*>(out + r * kp * P + (c / 64 * P + p) * 64 + c % 64) = f.p[p];
+            *reinterpret_cast<bf16x8*>(out + r * kp * P + (c / 64 * P + p) * 64 + c % 64) = v[p];
     }
 }
 
@@ -186,7 +187,7 @@ int launch(ForwardArgs<T> a, bool zp, hipStream_t stream) {
 
 template <int W, class T>
 int forward(ForwardArgs<T> a, const T* x, int64_t group, void* workspace, hipStream_t stream) {
-    constexpr int P = TokenFrag<T>::kParts;
+    constexpr int P = Tokens<T>::kParts;
     if (forward_workspace(P == 3 ? FQ_F32 : FQ_BF16, a.m, a.k)) {
         const int64_t kp = (a.k + 63) / 64 * 64;
         k_pieces<T><<<fqh::grid_all(a.m * kp / 8, 256), 256, 0, stream>>>(x, a.m, a.k, kp, (uint16_t*)workspace);

@@ -84,35 +84,61 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight token values as matrix operands: bfloat16 as they are; float32 as three
-// bfloat16 parts that sum to x exactly (each part takes the next 8 significant
-// bits by truncation, so no part overflows).  Inf and NaN stay in the first part.
+// 16 bytes at p of which `left` (may be <= 0) belong to the array, whose 16 bytes or
+// more end there: read from its end and moved down, zeros after.
+__device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t left) {
+    if (left >= 16) return load16(p);
+    if (left <= 0) return u32x4{0, 0, 0, 0};
+    const u32x4 v = load16(p + left - 16);
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    int bits = 8 * (16 - (int)left);  // 8 .. 120
+    if (bits >= 64) lo = hi, hi = 0, bits -= 64;
+    if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// Eight token values as they lie in memory, and as matrix operands: bfloat16 as they
+// are; float32 as three bfloat16 parts that sum to x exactly (each part takes the
+// next 8 significant bits by truncation, so no part overflows).  Inf and NaN stay in
+// the first part.  load_part reads the first n (may be <= 0) of the eight, the last
+// of a row of eight at least, from the row's end and moves them down; zeros after.
 template <class T>
-struct TokenFrag;
+struct Tokens;
 template <>
-struct TokenFrag<uint16_t> {
+struct Tokens<uint16_t> {
     static constexpr int kParts = 1;
-    bf16x8 p[1];
-    __device__ __forceinline__ void load(const uint16_t* s) { p[0] = __builtin_bit_cast(bf16x8, load16(s)); }
-    __device__ __forceinline__ void load_part(const uint16_t* s, int n) {  // the first n of 8, zeros after
-        uint32_t r[4] = {};
-        for (int i = 0; i < 8; ++i)
-            if (i < n) r[i / 2] |= (uint32_t)s[i] << (16 * (i & 1));
-        p[0] = __builtin_bit_cast(bf16x8, u32x4{r[0], r[1], r[2], r[3]});
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t* s) { v = load16(s); }
+    __device__ __forceinline__ void load_part(const uint16_t* s, int64_t n) {
+        v = load16_part(reinterpret_cast<const uint8_t*>(s), 2 * n);
     }
+    __device__ __forceinline__ void parts(bf16x8 (&p)[1]) const { p[0] = __builtin_bit_cast(bf16x8, v); }
 };
 template <>
-struct TokenFrag<float> {
+struct Tokens<float> {
     static constexpr int kParts = 3;
-    bf16x8 p[3];
-    __device__ __forceinline__ void split(const float (&f)[8]) {
+    u32x4 v[2];
+    __device__ __forceinline__ void load(const float* s) { v[0] = load16(s), v[1] = load16(s + 4); }
+    __device__ __forceinline__ void load_part(const float* s, int64_t n) {
+        if (n >= 8) return load(s);
+        v[0] = v[1] = u32x4{0, 0, 0, 0};
+        if (n <= 0) return;
+        const float* e = s + n - 8;
+        u32x4 a = load16(e), b = load16(e + 4);
+        const int by = 8 - (int)n;  // 1 .. 7
+        if (by & 4) a = b, b = u32x4{0, 0, 0, 0};
+        if (by & 2) a = u32x4{a[2], a[3], b[0], b[1]}, b = u32x4{b[2], b[3], 0, 0};
+        if (by & 1) a = u32x4{a[1], a[2], a[3], b[0]}, b = u32x4{b[1], b[2], b[3], 0};
+        v[0] = a, v[1] = b;
+    }
+    __device__ __forceinline__ void parts(bf16x8 (&p)[3]) const {
         uint32_t a[4], b[4], c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float r[2], s[2], h[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                h[j] = __builtin_canonicalizef(f[2 * i + j]);  // a NaN keeps a bit in its upper half
+                h[j] = __builtin_canonicalizef(__uint_as_float(v[i / 2][2 * (i % 2) + j]));  // a NaN keeps a bit in its upper half
                 const float top = __uint_as_float(__float_as_uint(h[j]) & 0xFFFF0000u);
                 r[j] = fabsf(h[j]) < INFINITY ? h[j] - top : 0.0f;
                 s[j] = r[j] - __uint_as_float(__float_as_uint(r[j]) & 0xFFFF0000u);
@@ -125,31 +151,7 @@ struct TokenFrag<float> {
         p[1] = __builtin_bit_cast(bf16x8, u32x4{b[0], b[1], b[2], b[3]});
         p[2] = __builtin_bit_cast(bf16x8, u32x4{c[0], c[1], c[2], c[3]});
     }
-    __device__ __forceinline__ void load(const float* s) {
-        const u32x4 u = load16(s), v = load16(s + 4);
-        const float f[8] = {__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3]),
-                            __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3])};
-        split(f);
-    }
-    __device__ __forceinline__ void load_part(const float* s, int n) {
-        float f[8];
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? s[i] : 0.0f;
-        split(f);
-    }
 };
-
-// 16 code bytes at p of which `left` (may be <= 0) belong to the weight, whose 16
-// bytes or more end there: read from its end and moved down, zeros after.
-__device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t left) {
-    if (left >= 16) return load16(p);
-    if (left <= 0) return u32x4{0, 0, 0, 0};
-    const u32x4 v = load16(p + left - 16);
-    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
-    int bits = 8 * (16 - (int)left);  // 8 .. 120
-    if (bits >= 64) lo = hi, hi = 0, bits -= 64;
-    if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
 
 // Host: columns per group sum of the kernels (128, 64 or 32; 0: the group size is
 // none that they take).  A group of at least the whole row never ends inside it.

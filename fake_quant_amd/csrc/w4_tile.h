@@ -3,11 +3,11 @@
 //
 // An operand tile lies in LDS in one of two layouts, both in 16-byte chunks of
 // eight bfloat16:
-//   by rows  [row][64 l], 8 chunks a row, chunk c of row r at c ^ (r & 7);
+//   by rows  [row][64 l], 8 chunks a row, chunk c of row r at c ^ (r / 2 & 7);
 //   by steps [64 l][row], chunk c of line l at by_steps(c, l): the source holds its
 //            rows as columns, and ds_read_b64_tr_b16 turns 4 x 16 blocks on the way
 //            to the matrix instruction.
-// Both permutations spread what one instruction reads or writes over all banks.
+// Both permutations spread the 256 bytes of a read cycle over all banks.
 // Dense operands arrive by buffer_load ... lds (no registers, out-of-range chunks
 // arrive as zeros); stored 4-bit weights pass through registers, where they
 // become bfloat16.  Two stages: the next one fills while the present one is used.
@@ -35,7 +35,7 @@ struct Shape {
     static constexpr int MS = BM / WM / 32, NS = BN / WN / 32;  // 32 x 32 tiles of a wave
 };
 
-__device__ __forceinline__ int by_rows(int row, int chunk) { return row * 64 + ((chunk ^ (row & 7)) * 8); }
+__device__ __forceinline__ int by_rows(int row, int chunk) { return row * 64 + ((chunk ^ (row / 2 & 7)) * 8); }
 // position of chunk c in line l, and the chunk at a position
 __device__ __forceinline__ int by_steps(int c, int l) {
     return c ^ ((l & 1) << 2) ^ (l & 2) ^ ((l & 2) << 2) ^ ((c >> 3) & 3);
@@ -74,6 +74,7 @@ template <int ROWS, int THREADS>
 struct DenseRows {
     static constexpr int kLoads = ROWS * 8 / THREADS, kWaveRows = kLoads * 8;
     const uint16_t* base;
+    static_assert(kLoads % 2 == 0, "8 rows a load: even and odd loads differ in row / 2 & 4");
     uint32_t bytes, off, step;
     int64_t cols;
     int col, wave;
@@ -83,16 +84,17 @@ struct DenseRows {
         const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
         base = p + row0 * ld;
         bytes = (uint32_t)(left * ld * 2);
-        col = ((lane % 8) ^ (lane / 8)) * 8;
-        off = (uint32_t)((wave * kWaveRows + lane / 8) * ld + col) * 2;
+        col = ((lane % 8) ^ (lane / 16)) * 8;
+        off = (uint32_t)((wave * kWaveRows + lane / 8) * ld) * 2;
         step = (uint32_t)(8 * ld * 2);
     }
     __device__ __forceinline__ void fill(uint16_t* tile, int64_t l0) const {
         const u32x4 b = buffer(base + l0, bytes);
-        const bool in = col < cols - l0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            dma16(b, tile + (wave * kWaveRows + i * 8) * 64, in ? off + i * step : kOut);
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = i % 2 ? col ^ 32 : col;
+            dma16(b, tile + (wave * kWaveRows + i * 8) * 64, c < cols - l0 ? off + i * step + 2 * c : kOut);
+        }
     }
 };
 
