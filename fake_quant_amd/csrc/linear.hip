@@ -202,7 +202,7 @@ int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int
     const size_t need = fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
     if (few_tokens(m, n, k, group)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
-    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)))
+    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(y, n, elem(dtype)))
         return forward_matmul(x, dtype, m, n, k, group, *w, y, workspace, stream);
     return dtype == FQ_F32 ? matmul<float>(x, m, n, k, group, *w, y, stream)
                            : matmul<uint16_t>(x, m, n, k, group, *w, y, stream);
@@ -220,7 +220,8 @@ int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int6
     const size_t need = fql_w4_gated_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
     if (few_tokens(m, n, k, group)) return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
-    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)))
+    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(h, n, elem(dtype)) &&
+        stored_whole(g, n, elem(dtype)) && stored_whole(u, n, elem(dtype)))
         return forward_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, workspace, stream);
     return dtype == FQ_F32 ? gated<float>(x, m, n, k, group, act, *gate, *up, h, g, u, stream)
                            : gated<uint16_t>(x, m, n, k, group, act, *gate, *up, h, g, u, stream);

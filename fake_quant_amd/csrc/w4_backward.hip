@@ -20,6 +20,9 @@ struct DxArgs {
     uint16_t* dx;
     int64_t m, n, k;
     uint32_t ni, nj;
+    // one weight of a pair may have no zero-points: then any readable words, masked to zeros
+    const int32_t* zp[2];
+    int32_t mask[2];
 };
 template <class T>
 struct DwArgs {
@@ -32,71 +35,83 @@ struct DwArgs {
 };
 
 // The weights' side of a tile, 64 rows by BN columns: a thread holds 32 codes of a row.
+struct CodeRegs {
+    u32x4 c;
+    float s;
+    int32_t z, mask;
+    bool none;
+};
 template <int BN, bool ZP>
 struct CodeSteps {
-    static constexpr int kParts = BN / 32;
+    static constexpr int kParts = BN / 32, kLoads = ZP ? 3 : 2;
     const DxArgs& a;
-    int64_t byte, gi;
+    int64_t byte, gi, l0 = 0;
     int line, part;
-    u32x4 c;
-    float s, z;
     __device__ __forceinline__ CodeSteps(const DxArgs& a_, int64_t col0, int t) : a(a_), line(t / kParts), part(t % kParts) {
         const int64_t col = col0 + 32 * part;
         byte = col / 2;
         gi = (col < a.k ? col : a.k - 1) / a.w[0].group;
     }
-    __device__ __forceinline__ void load(int64_t l0) {
-        const int which = l0 >= a.run;  // a step lies in one of the matrices
-        const W4Mat& w = a.w[which];
-        const int64_t r = l0 - (which ? a.run : 0) + line, at = r < a.n ? r : a.n - 1;
-        c = load16_part(w.codes + at * w.row_bytes + byte, (a.n - at) * w.row_bytes - byte);
-        s = r < a.n ? w.scale[at * w.ng + gi] * 16.0f : 0.0f;
-        if constexpr (ZP) z = w.zp ? (float)w.zp[at * w.ng + gi] * 0.0625f : 0.0f;
-        else z = 0.0f;
+    // The thread's row at step l0, and the bytes of the matrix from its codes there on.
+    __device__ __forceinline__ int64_t row_at(int64_t step, int64_t& left) const {
+        const int64_t r = step - (step >= a.run ? a.run : 0) + line, at = r < a.n ? r : a.n - 1;
+        left = (a.n - at) * a.w[0].row_bytes - byte;
+        return r;
     }
-    __device__ __forceinline__ void store(uint16_t* tile) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<bf16x8*>(tile + line * BN + by_steps(4 * part + j, line) * 8) = weights_bf16<ZP>(c[j], z, s);
+    // The codes of the present step; then the next one is present.  Nothing here reads
+    // what was loaded: that would wait for it.
+    __device__ __forceinline__ void load(CodeRegs& d) {
+        const int which = l0 >= a.run;  // a step lies in one of the matrices
+        int64_t left;
+        const int64_t r = row_at(l0, left), at = r < a.n ? r : a.n - 1;
+        // past the matrix a thread reads its last 16 bytes, which whole() puts in place
+        d.c = load16(a.w[which].codes + at * a.w[0].row_bytes + (left < 16 ? byte + left - 16 : byte));
+        d.s = a.w[which].scale[at * a.w[0].ng + gi];
+        if constexpr (ZP) d.z = a.zp[which][at * a.w[0].ng + gi], d.mask = a.mask[which];
+        d.none = r >= a.n;
+        l0 += kDeep;
+    }
+    // Puts in place what the last load() read.
+    __device__ __forceinline__ void whole(CodeRegs& d) const {
+        int64_t left;
+        row_at(l0 - kDeep, left);
+        if (left < 16) d.c = drop_bytes(d.c, left <= 0 ? 16 : 16 - (int)left);
+    }
+    // Codes 8 J .. of those to a tile.
+    template <int J>
+    __device__ __forceinline__ void store(uint16_t* tile, const CodeRegs& d) const {
+        *reinterpret_cast<bf16x8*>(tile + line * BN + by_steps(4 * part + J, line) * 8) =
+            weights_bf16<ZP>(d.c[J], ZP ? (float)(d.z & d.mask) * 0.0625f : 0.0f, d.none ? 0.0f : d.s * 16.0f);
     }
 };
 
-// A tile's sums to rows i0 .. of a matrix of k columns.  Lanes hold one row each and
-// runs of four columns: they meet in LDS, so that memory sees whole rows.
-template <class S, class T, class Row>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::MS][S::NS], T* lds, int64_t j0, int64_t k, Row row) {
-    constexpr int kPasses = sizeof(T) / 2, kRows = S::BM / kPasses, kPitch = S::BN + 16 / sizeof(T);
-    constexpr int kVec = 16 / sizeof(T), kWide = S::BN / kVec;
-    static_assert(kPasses == 1 || kPasses == S::WM, "a pass takes whole waves");
-    const int t = threadIdx.x, lane = t % 64, wave = t / 64;
-    const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
-    const bool whole = k % kVec == 0;
+// A wave's sums to its rows and columns of a tile in LDS: lanes hold one row each and runs of four columns.
+template <class S, class T>
+__device__ __forceinline__ void put_sums(const f32x16 (&acc)[S::MS][S::NS], T* lds, int pitch) {
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    T* at = lds + (wave / S::WN * (S::MS * 32) + lane % 32) * pitch + wave % S::WN * (S::NS * 32) + 4 * (lane / 32);
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        if (p) __syncthreads();
-        if (kPasses == 1 || wave / S::WN == p)
+    for (int i = 0; i < S::MS; ++i)
 #pragma unroll
-            for (int i = 0; i < S::MS; ++i)
+        for (int j = 0; j < S::NS; ++j)
 #pragma unroll
-                for (int j = 0; j < S::NS; ++j)
+            for (int e = 0; e < 16; ++e) store_f(at + 32 * i * pitch + 32 * j + e / 4 * 8 + e % 4, acc[i][j][e]);
+}
+
+// Operand registers of half a step, and their products.
+template <class S>
+struct Frags {
+    bf16x8 a[S::MS][2], b[S::NS][2];
+};
+template <class S>
+__device__ __forceinline__ void multiply(f32x16 (&acc)[S::MS][S::NS], const Frags<S>& f) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        T* d = lds + (wi - p * kRows + 32 * i + lane % 32) * kPitch + wj + 32 * j + 2 * e + 4 * (lane / 32);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) store_f(d + f, acc[i][j][e + f]);
-                    }
-        __syncthreads();
-        for (int v = t; v < kRows * kWide; v += S::kThreads) {
-            const int r = v / kWide, c = v % kWide * kVec;
-            T* out = row(p * kRows + r);
-            if (!out || j0 + c >= k) continue;
-            const T* s = lds + r * kPitch + c;
-            if (whole) *reinterpret_cast<u32x4*>(out + j0 + c) = *reinterpret_cast<const u32x4*>(s);
-            else
-                for (int f = 0; f < kVec; ++f)
-                    if (j0 + c + f < k) out[j0 + c + f] = s[f];
-        }
-    }
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
 }
 
 template <class S, class T>
@@ -105,53 +120,76 @@ struct TileLds {
         struct {
             __attribute__((aligned(1024))) uint16_t a[2][S::BM * kDeep], b[2][S::BN * kDeep];
         };
-        T out[S::BM * 2 / sizeof(T) * (S::BN + 16 / sizeof(T))];
+        T out[OutTile<S, T, S::BN>::kSize];
     };
 };
 
-template <class S, bool ZP>
+// RAGGED: k is no multiple of 32, so that a thread's run of codes may end inside the
+// matrix (a branch that costs the others 30%: 177 against 135 us at 4096^3).
+template <class S, bool ZP, bool RAGGED>
 __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     __shared__ TileLds<S, uint16_t> lds;
     const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
     uint32_t ti, tj;
     tile_at(blockIdx.x, a.ni, a.nj, ti, tj);
     const int64_t i0 = (int64_t)ti * S::BM, j0 = (int64_t)tj * S::BN;
-    const DenseRows<S::BM, S::kThreads> ys(a.dy, i0, a.m, a.ld, a.cols, wave, lane);
+    DenseRows<S::BM, S::kThreads> ys(a.dy, i0, a.m, a.ld, a.cols, wave, lane);
     CodeSteps<S::BN, ZP> ws(a, j0, t);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
     const uint32_t steps = (uint32_t)((a.cols + kDeep - 1) / kDeep);
 
     f32x16 acc[S::MS][S::NS] = {};
-    ws.load(0);
-    ws.store(lds.b[0]);
-    ys.fill(lds.a[0], 0);
-    if (1 < steps) ws.load(kDeep);
-    wait_dma();
+    Frags<S> f[2];
+    CodeRegs c, ahead;
+    const uint32_t at[2] = {lds_address(lds.a[0]), lds_address(lds.a[1])};
+    const auto read = [&](Frags<S>& d, int stage, int half) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j) d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
+#pragma unroll
+            for (int i = 0; i < S::MS; ++i) d.a[i][h] = frag_rows(lds.a[stage], wi + 32 * i, 2 * half + h, lane);
+        }
+    };
+    const auto stage = [&](int cur) {
+        ws.load(ahead);
+        __builtin_amdgcn_sched_barrier(0);  // not behind the products, where it would be waited for
+        read(f[1], cur, 1);
+        ws.template store<2>(lds.b[cur ^ 1], c);
+        ws.template store<3>(lds.b[cur ^ 1], c);
+        multiply<S>(acc, f[0]);
+        wait_loads();
+        if constexpr (RAGGED) ws.whole(ahead);
+        __syncthreads();  // the other stage is full, and this one has been read
+        c = ahead;
+        ys.fill(at[cur]);
+        read(f[0], cur ^ 1, 0);
+        ws.template store<0>(lds.b[cur], c);
+        ws.template store<1>(lds.b[cur], c);
+        multiply<S>(acc, f[1]);
+    };
+    ws.load(c);
+    if constexpr (RAGGED) ws.whole(c);
+    ws.load(ahead);
+    ys.fill(at[0]);
+    ws.template store<0>(lds.b[0], c);
+    ws.template store<1>(lds.b[0], c);
+    ws.template store<2>(lds.b[0], c);
+    ws.template store<3>(lds.b[0], c);
+    if constexpr (RAGGED) ws.whole(ahead);
+    wait_loads();
     __syncthreads();
-    for (uint32_t st = 0; st < steps; ++st) {
-        const int cur = st & 1;
-        if (st + 1 < steps) {
-            ws.store(lds.b[cur ^ 1]);
-            ys.fill(lds.a[cur ^ 1], (int64_t)(st + 1) * kDeep);
-            if (st + 2 < steps) ws.load((int64_t)(st + 2) * kDeep);
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            bf16x8 f[S::MS], b[S::NS];
-#pragma unroll
-            for (int j = 0; j < S::NS; ++j) b[j] = frag_steps<S::BN>(lds.b[cur], wj + 32 * j, d, lane);
-#pragma unroll
-            for (int i = 0; i < S::MS; ++i) f[i] = frag_rows(lds.a[cur], wi + 32 * i, d, lane);
-#pragma unroll
-            for (int i = 0; i < S::MS; ++i)
-#pragma unroll
-                for (int j = 0; j < S::NS; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], f[i], acc[i][j], 0, 0, 0);
-        }
-        wait_dma();
-        __syncthreads();
-    }
-    store_tile<S>(acc, lds.out, j0, a.k, [&](int r) { return i0 + r < a.m ? a.dx + (i0 + r) * a.k : nullptr; });
+    c = ahead;
+    ys.fill(at[1]);
+    read(f[0], 0, 0);
+    ws.template store<0>(lds.b[1], c);
+    ws.template store<1>(lds.b[1], c);
+    for (uint32_t st = 0; st < steps; ++st) stage(st & 1);
+    wait_loads();
+    __syncthreads();
+    OutTile<S, uint16_t, S::BN>::store(
+        lds.out, j0, a.k, [&](uint16_t* out, int pitch) { put_sums<S>(acc, out, pitch); },
+        [&](int r) { return i0 + r < a.m ? a.dx + (i0 + r) * a.k : nullptr; });
 }
 
 template <class S, class T>
@@ -161,42 +199,53 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
     uint32_t ti, tj;
     tile_at(blockIdx.x, a.ni, a.nj, ti, tj);
     const int64_t i0 = (int64_t)ti * S::BM, j0 = (int64_t)tj * S::BN;
-    const DenseSteps<S::BM, S::kThreads> ys(a.dy, i0, a.cols, a.m, a.ld, wave, lane);
-    const DenseSteps<S::BN, S::kThreads> xs(a.x, j0, a.ldx, a.m, a.ldx, wave, lane);
+    DenseSteps<S::BM, S::kThreads> ys(a.dy, i0, a.cols, a.m, a.ld, wave, lane);
+    DenseSteps<S::BN, S::kThreads> xs(a.x, j0, a.ldx, a.m, a.ldx, wave, lane);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
     const uint32_t steps = (uint32_t)((a.m + kDeep - 1) / kDeep);
 
     f32x16 acc[S::MS][S::NS] = {};
-    ys.fill(lds.a[0], 0);
-    xs.fill(lds.b[0], 0);
-    wait_dma();
+    Frags<S> f[2];
+    const auto read = [&](Frags<S>& d, int stage, int half) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j) d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
+#pragma unroll
+            for (int i = 0; i < S::MS; ++i) d.a[i][h] = frag_steps<S::BM>(lds.a[stage], wi + 32 * i, 2 * half + h, lane);
+        }
+    };
+    const uint32_t at[2] = {lds_address(lds.a[0]), lds_address(lds.a[1])};
+    const uint32_t bt[2] = {lds_address(lds.b[0]), lds_address(lds.b[1])};
+    ys.fill(at[0]);
+    xs.fill(bt[0]);
+    wait_loads();
     __syncthreads();
-    for (uint32_t st = 0; st < steps; ++st) {
-        const int cur = st & 1;
-        if (st + 1 < steps) {
-            ys.fill(lds.a[cur ^ 1], (int64_t)(st + 1) * kDeep);
-            xs.fill(lds.b[cur ^ 1], (int64_t)(st + 1) * kDeep);
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            bf16x8 f[S::MS], b[S::NS];
-#pragma unroll
-            for (int j = 0; j < S::NS; ++j) b[j] = frag_steps<S::BN>(lds.b[cur], wj + 32 * j, d, lane);
-#pragma unroll
-            for (int i = 0; i < S::MS; ++i) f[i] = frag_steps<S::BM>(lds.a[cur], wi + 32 * i, d, lane);
-#pragma unroll
-            for (int i = 0; i < S::MS; ++i)
-#pragma unroll
-                for (int j = 0; j < S::NS; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], f[i], acc[i][j], 0, 0, 0);
-        }
-        wait_dma();
-        __syncthreads();
+    ys.fill(at[1]);
+    xs.fill(bt[1]);
+    read(f[0], 0, 0);
+    const auto stage = [&](int cur) {
+        read(f[1], cur, 1);
+        multiply<S>(acc, f[0]);
+        wait_loads();
+        __syncthreads();  // the other stage is full, and this one has been read
+        ys.fill(at[cur]);
+        xs.fill(bt[cur]);
+        read(f[0], cur ^ 1, 0);
+        multiply<S>(acc, f[1]);
+    };
+    for (uint32_t st = 0; st < steps; st += 2) {  // past the end both operands are zeros
+        stage(0);
+        stage(1);
     }
-    store_tile<S>(acc, lds.out, j0, a.k, [&](int r) -> T* {
-        const int64_t i = i0 + r, f = i < a.run ? i : i - a.run;
-        return i < a.cols && f < a.n ? a.dw[i < a.run ? 0 : 1] + f * a.k : nullptr;
-    });
+    wait_loads();
+    __syncthreads();
+    OutTile<S, T, S::BN>::store(
+        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch); },
+        [&](int r) -> T* {
+            const int64_t i = i0 + r, f = i < a.run ? i : i - a.run;
+            return i < a.cols && f < a.n ? a.dw[i < a.run ? 0 : 1] + f * a.k : nullptr;
+        });
 }
 
 // dg and du beside each other: out [m][2 run], zeros in columns n .. run - 1 of each half.
@@ -251,9 +300,13 @@ int launch_dx(DxArgs a, bool zp, hipStream_t stream) {
     const int64_t ni = (a.m + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
     if (ni * nj > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
     a.ni = (uint32_t)ni, a.nj = (uint32_t)nj;
+    for (int i = 0; i < 2; ++i) {
+        a.zp[i] = a.w[i].zp ? a.w[i].zp : reinterpret_cast<const int32_t*>(a.w[i].scale);
+        a.mask[i] = a.w[i].zp ? -1 : 0;
+    }
     const dim3 g((unsigned)(ni * nj)), b(S::kThreads);
-    if (zp) k_dx<S, true><<<g, b, 0, stream>>>(a);
-    else k_dx<S, false><<<g, b, 0, stream>>>(a);
+    if (a.k % 32) zp ? k_dx<S, true, true><<<g, b, 0, stream>>>(a) : k_dx<S, false, true><<<g, b, 0, stream>>>(a);
+    else zp ? k_dx<S, true, false><<<g, b, 0, stream>>>(a) : k_dx<S, false, false><<<g, b, 0, stream>>>(a);
     return fqh::launched();
 }
 template <class S, class T>

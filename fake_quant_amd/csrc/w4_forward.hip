@@ -20,139 +20,190 @@ struct ForwardArgs {
     W4Mat w[2];
     T* out[3];  // y, or h, g, u
     int64_t m, n, k;
-    uint32_t spans, per_group;  // spans in a row, spans in a group
-    uint32_t ni, nj;            // tiles
+    uint32_t spans, inverse;  // spans in a row; ceil(2^31 / spans in a group)
+    uint32_t ni, nj;          // tiles
     int act;
+    // one weight of a pair may have no zero-points: then any readable words, masked to zeros
+    const int32_t* zp[2];
+    int32_t mask[2];
 };
 
 // The weights' side of a tile: a thread holds 32 codes of one of the tile's rows.
+struct CodeRegs {
+    u32x4 c;
+    float s;
+    int32_t z;
+    bool none;
+};
 template <int BN, int SPAN, bool ZP, int W>
 struct CodeRows {
-    const uint8_t* p;
+    // the tile's first row of the matrix (one per wave), and the thread's offsets from there
+    const uint8_t* codes;
     const float* scale;
     const int32_t* zp;
-    int64_t left;  // bytes of the matrix from p on
-    uint32_t spans, per_group;
+    uint32_t at, group, end;  // end: offset of the matrix's last 16 bytes, if that near
+    uint32_t spans, inverse, step = 0, part = 0, loaded = 0, parts, steps;
+    int32_t mask;
     int row, half;
-    u32x4 c;
-    float s, z;
     template <class Args>
     __device__ __forceinline__ CodeRows(const Args& a, int64_t col0, int t)
-        : spans(a.spans), per_group(a.per_group), row(t / 2), half(t % 2) {
-        // a wave's 64 rows hold 32 of the gate matrix and then the same 32 of the up matrix
-        const W4Mat& w = a.w[W == 1 ? 0 : row / 32 % 2];
-        int64_t r = col0 + (W == 1 ? row : row / 64 * 32 + row % 32);
-        r = r < a.n ? r : a.n - 1;
-        p = w.codes + r * w.row_bytes + half * 16;
-        left = (a.n - r) * w.row_bytes - half * 16;
-        scale = w.scale + r * w.ng;
-        zp = w.zp ? w.zp + r * w.ng : nullptr;
+        : spans(a.spans), inverse(a.inverse), parts(a.parts), steps((uint32_t)((a.k + kDeep - 1) / kDeep)), row(t / 2), half(t % 2) {
+        // a wave's 64 rows of the tile hold 32 of the gate matrix and then the same 32 of the up matrix
+        const int which = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(row / 32 % 2);
+        const W4Mat& w = a.w[which];
+        const int64_t last = a.n - 1 - col0, bytes = (a.n - col0) * w.row_bytes - 16;
+        int r = W == 1 ? row : row / 64 * 32 + row % 32;
+        r = r < last ? r : (int)last;
+        codes = w.codes + col0 * w.row_bytes;
+        scale = w.scale + col0 * w.ng;
+        zp = a.zp[which] + col0 * w.ng;
+        mask = a.mask[which];
+        at = (uint32_t)(r * w.row_bytes + half * 16);
+        group = (uint32_t)(r * w.ng);
+        end = bytes < (1 << 30) ? (uint32_t)bytes : 1u << 30;
     }
-    __device__ __forceinline__ void load(uint32_t step) {
-        const int64_t b = (int64_t)step * 32;
-        // past its row's end a thread reads codes of the next row, which meet zeros of x
-        c = load16_part(p + b, left - b);
+    // The codes of the present step; then the next one is present (each comes `parts`
+    // times).  Nothing here reads what was loaded: that would wait for it.
+    __device__ __forceinline__ void load(CodeRegs& d) {
+        // past its row's end a thread reads codes of the next row, which meet zeros of
+        // x, and past the matrix its last 16 bytes, which whole() puts in place
+        const uint32_t b = at + step * 32;
+        d.c = load16(codes + (b < end ? b : end));
+        loaded = step;
         uint32_t i = SPAN == 64 ? step : 2 * step + half;
-        i = i < spans ? i : spans - 1;
-        if (per_group > 1) i /= per_group;
-        s = scale[i];
-        if constexpr (ZP) z = zp ? (float)zp[i] : 0.0f;
+        i = group + (uint32_t)((uint64_t)(i < spans ? i : spans - 1) * inverse >> 31);  // as in the few-token kernel
+        d.s = scale[i];
+        if constexpr (ZP) d.z = zp[i];
+        d.none = step >= steps;
+        if (++part == parts) part = 0, ++step;
     }
-    __device__ __forceinline__ void store(uint16_t* tile, float* scales) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<bf16x8*>(tile + by_rows(row, half * 4 + j)) = codes_bf16<ZP>(c[j], ZP ? z * 0.0625f : 0.0f);
-        if (SPAN == 32 || half == 0) scales[(SPAN == 32 ? half * BN : 0) + row] = s * 16.0f;
+    // Puts in place what the last load() read.
+    __device__ __forceinline__ void whole(CodeRegs& d) const {
+        const int past = (int)(at + loaded * 32 - end);
+        d.c = drop_bytes(d.c, past < 0 ? 0 : past < 16 ? past : 16);
+    }
+    // the thread's first chunk in the tile at LDS address `tile`: chunk j is at this ^ 16 j
+    __device__ __forceinline__ uint32_t place(uint32_t tile) const { return tile + 2 * by_rows(row, half * 4); }
+    __device__ __forceinline__ void store(uint32_t at, int j, const CodeRegs& d) const {
+        lds_write(at ^ 16 * j, codes_bf16<ZP>(d.c[j], ZP ? (float)(d.z & mask) * 0.0625f : 0.0f));
+    }
+    __device__ __forceinline__ void store_scale(float* scales, const CodeRegs& d) const {
+        scales[(SPAN == 32 ? half * BN : 0) + row] = d.none ? 0.0f : d.s * 16.0f;  // SPAN 64: both halves have the same
     }
 };
+
+__device__ __forceinline__ void add(f32x16& acc, const f32x16& p, float s) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = fmaf(p[e], s, acc[e]);
+}
 
 template <class S, int SPAN, bool ZP, int W, class T>
 __global__ __launch_bounds__(S::kThreads, 2) void k_forward(ForwardArgs<T> a) {
     constexpr int BM = S::BM, BN = S::BN, kSums = kDeep / SPAN;
-    __shared__ __attribute__((aligned(1024))) uint16_t xa[2][BM * kDeep];
-    __shared__ __attribute__((aligned(1024))) uint16_t wb[2][BN * kDeep];
-    __shared__ float sc[2][kSums * BN];
+    using Out = OutTile<S, T, BN / W>;
+    __shared__ union {
+        struct {
+            __attribute__((aligned(1024))) uint16_t x[2][BM * kDeep], w[2][BN * kDeep];
+            float s[2][kSums * BN];
+        };
+        T out[Out::kSize];
+    } lds;
+    auto& sc = lds.s;
     const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
     uint32_t ti, tj;
     tile_at(blockIdx.x, a.ni, a.nj, ti, tj);
     const int64_t i0 = (int64_t)ti * BM, j0 = (int64_t)tj * (BN / W);
-    const DenseRows<BM, S::kThreads> xs(a.x, i0, a.m, a.ld, a.cols, wave, lane);
+    DenseRows<BM, S::kThreads> xs(a.x, i0, a.m, a.ld, a.cols, wave, lane);
     CodeRows<BN, SPAN, ZP, W> ws(a, j0, t);
-    const uint32_t steps = (uint32_t)((a.cols + kDeep - 1) / kDeep), parts = a.parts;
+    const uint32_t steps = (uint32_t)((a.cols + kDeep - 1) / kDeep);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
 
+    const bool ragged = a.k % kDeep != 0;
     f32x16 acc[S::MS][S::NS] = {};
-    ws.load(0);
-    xs.fill(xa[0], 0);
-    ws.store(wb[0], sc[0]);
-    uint32_t kt = 0, part = 0;  // step of W, part of x, of the codes in registers
-    auto advance = [&] {
-        if (++part == parts) part = 0, ++kt;
-    };
-    advance();
-    if (1 < steps) ws.load(kt);
-    wait_dma();
-    __syncthreads();
-    for (uint32_t st = 0; st < steps; ++st) {
-        const int cur = st & 1;
-        if (st + 1 < steps) {
-            ws.store(wb[cur ^ 1], sc[cur ^ 1]);  // before new loads, which its wait would include
-            xs.fill(xa[cur ^ 1], (int64_t)(st + 1) * kDeep);
-            advance();
-            if (st + 2 < steps) ws.load(kt);
-        }
-        bf16x8 b[S::NS][4];
+    CodeRegs c, ahead;
+    constexpr uint32_t kStageX = BM * kDeep * 2, kStageW = BN * kDeep * 2;
+    const uint32_t xat = lds_address(lds.x), wat = lds_address(lds.w);
+    const uint32_t xread = frag_rows_at(xat, wi, lane), wread = frag_rows_at(wat, wj, lane), wwrite = ws.place(wat);
+    const auto stage = [&](int cur) {
+        if (ragged) ws.whole(c);
+        bf16x8 b[S::NS][4], f[4];
         float s[kSums][S::NS];
+        const uint32_t xr = hidden(xread + cur * kStageX), wr = hidden(wread + cur * kStageW);
+        const uint32_t wt = hidden(wwrite + (cur ^ 1) * kStageW);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) f[d] = lds_read(xr ^ 32 * d);
 #pragma unroll
         for (int j = 0; j < S::NS; ++j) {
 #pragma unroll
-            for (int d = 0; d < 4; ++d) b[j][d] = frag_rows(wb[cur], wj + 32 * j, d, lane);
+            for (int d = 0; d < 4; ++d) b[j][d] = lds_read((wr ^ 32 * d) + 4096 * j);
 #pragma unroll
             for (int g = 0; g < kSums; ++g) s[g][j] = sc[cur][g * BN + wj + 32 * j + lane % 32];
         }
 #pragma unroll
         for (int i = 0; i < S::MS; ++i) {
-            bf16x8 f[4];
-#pragma unroll
-            for (int d = 0; d < 4; ++d) f[d] = frag_rows(xa[cur], wi + 32 * i, d, lane);
 #pragma unroll
             for (int g = 0; g < kSums; ++g)
 #pragma unroll
                 for (int j = 0; j < S::NS; ++j) {
                     f32x16 p = {};
 #pragma unroll
-                    for (int d = g * (4 / kSums); d < (g + 1) * (4 / kSums); ++d)
+                    for (int d = g * (4 / kSums); d < (g + 1) * (4 / kSums); ++d) {
                         p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[d], b[j][d], p, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(p[e], s[g][j], acc[i][j][e]);
+                        if (j == S::NS - 1 && i + 1 < S::MS) f[d] = lds_read((xr ^ 32 * d) + 4096 * (i + 1));
+                    }
+                    add(acc[i][j], p, s[g][j]);
                 }
-        }
-        wait_dma();
-        __syncthreads();
-    }
-
-#pragma unroll
-    for (int i = 0; i < S::MS; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int64_t r = i0 + wi + 32 * i + 8 * (e / 4) + 4 * (lane / 32) + e % 4;
-            if (r >= a.m) continue;
-            if constexpr (W == 1) {
-#pragma unroll
-                for (int j = 0; j < S::NS; ++j) {
-                    const int64_t c = j0 + wj + 32 * j + lane % 32;
-                    if (c < a.n) store_f(a.out[0] + r * a.n + c, acc[i][j][e]);
-                }
-            } else {
-                const int64_t c = j0 + wj / 2 + lane % 32, at = r * a.n + c;
-                if (c >= a.n) continue;
-                store_f(a.out[0] + at, act_value(a.act, acc[i][0][e]) * acc[i][1][e]);
-                if (a.out[1]) {
-                    store_f(a.out[1] + at, acc[i][0][e]);
-                    store_f(a.out[2] + at, acc[i][1][e]);
-                }
+            if (i == 0) {  // early, but behind the first products, which need nothing but LDS
+                ws.load(ahead);
+                xs.fill(xat + (cur ^ 1) * kStageX);  // zeros past the end
             }
+            // the next step's codes become integers beside the products
+#pragma unroll
+            for (int d = i * 4 / S::MS; d < (i + 1) * 4 / S::MS; ++d) ws.store(wt, d, c);
+            __builtin_amdgcn_sched_barrier(0);  // neither all sums at once nor loads that are waited for
         }
+        ws.store_scale(sc[cur ^ 1], c);
+        wait_loads();
+        __syncthreads();
+        c = ahead;
+    };
+    ws.load(c);
+    if (ragged) ws.whole(c);
+    ws.load(ahead);
+    xs.fill(xat);
+    for (int d = 0; d < 4; ++d) ws.store(wwrite, d, c);
+    ws.store_scale(sc[0], c);
+    wait_loads();
+    __syncthreads();
+    c = ahead;
+    for (uint32_t st = 0; st < steps; ++st) stage(st & 1);
+
+    // lanes hold one column each and runs of four rows
+    const auto store = [&](T* to, auto value) {
+        Out::store(
+            lds.out, j0, a.n,
+            [&](T* out, int pitch) {
+                T* at = out + (wi + 4 * (lane / 32)) * pitch + wj / W + lane % 32;
+#pragma unroll
+                for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NS / W; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            store_f(at + (32 * i + e / 4 * 8 + e % 4) * pitch + 32 * j, value(i, j, e));
+            },
+            [&](int r) { return i0 + r < a.m ? to + (i0 + r) * a.n : nullptr; });
+    };
+    if constexpr (W == 1) {
+        store(a.out[0], [&](int i, int j, int e) { return acc[i][j][e]; });
+    } else {
+        static_assert(S::NS == 2, "a wave holds 32 columns of both matrices");
+        if (a.out[1]) {
+            store(a.out[1], [&](int i, int, int e) { return acc[i][0][e]; });
+            store(a.out[2], [&](int i, int, int e) { return acc[i][1][e]; });
+        }
+        store(a.out[0], [&](int i, int, int e) { return act_value(a.act, acc[i][0][e]) * acc[i][1][e]; });
+    }
 }
 
 // x as the kernel reads it: [m][pieces of 64 columns][PARTS][64] bfloat16, zeros
@@ -201,7 +252,12 @@ int forward(ForwardArgs<T> a, const T* x, int64_t group, void* workspace, hipStr
     const bool fine = !(group >= a.k || group % 64 == 0), zp = a.w[0].zp || a.w[W - 1].zp;
     const int span = fine ? 32 : 64;
     a.spans = (uint32_t)((a.k + span - 1) / span);
-    a.per_group = spans_per_group(group, a.k, span);
+    const uint32_t per = spans_per_group(group, a.k, span);
+    a.inverse = (uint32_t)((((uint64_t)1 << 31) + per - 1) / per);
+    for (int i = 0; i < 2; ++i) {
+        a.zp[i] = a.w[i].zp ? a.w[i].zp : reinterpret_cast<const int32_t*>(a.w[i].scale);
+        a.mask[i] = a.w[i].zp ? -1 : 0;
+    }
     using Big = Shape<256, 256, 2, 4>;
     using Small = Shape<128, 128, 2, 2>;
     const int64_t big = ((a.m + 255) / 256) * ((a.n * W + 255) / 256);

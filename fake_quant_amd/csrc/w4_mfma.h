@@ -84,17 +84,21 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 v) {
     return u32x4{c[0], c[1], d[0], d[1]};
 }
 
+// The upper 16 - n of 16 bytes, moved down, zeros after (n: 0 .. 16).
+__device__ __forceinline__ u32x4 drop_bytes(u32x4 v, int n) {
+    if (n >= 16) return u32x4{0, 0, 0, 0};
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    int bits = 8 * n;
+    if (bits >= 64) lo = hi, hi = 0, bits -= 64;
+    if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
 // 16 bytes at p of which `left` (may be <= 0) belong to the array, whose 16 bytes or
 // more end there: read from its end and moved down, zeros after.
 __device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t left) {
     if (left >= 16) return load16(p);
     if (left <= 0) return u32x4{0, 0, 0, 0};
-    const u32x4 v = load16(p + left - 16);
-    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
-    int bits = 8 * (16 - (int)left);  // 8 .. 120
-    if (bits >= 64) lo = hi, hi = 0, bits -= 64;
-    if (bits) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    return drop_bytes(load16(p + left - 16), 16 - (int)left);
 }
 
 // Eight token values as they lie in memory, and as matrix operands: bfloat16 as they

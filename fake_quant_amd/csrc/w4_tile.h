@@ -48,53 +48,68 @@ __device__ __forceinline__ int by_steps_at(int p, int l) {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// A buffer of `bytes` bytes from p on: loads beyond its end give zeros.  Uniform over the wave.
+// A buffer of `bytes` bytes from p on: loads beyond its end give zeros.  Uniform over
+// the wave; the wait states (5) cover scalar registers that the vector unit has just
+// written and a load that dma16 hides from the compiler reads.
 __device__ __forceinline__ u32x4 buffer(const void* p, uint32_t bytes) {
     const uint64_t a = (uint64_t)p;
-    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)a),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xFFFF),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+    u32x4 b{(uint32_t)__builtin_amdgcn_readfirstlane((int)a),
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32) & 0xFFFF),
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+    asm volatile("s_nop 4" : "+s"(b));
+    return b;
 }
-// 16 bytes a lane from offset `off` of a buffer to 1 KiB of LDS at dst (one address per
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)p);
+}
+// 16 bytes a lane from offset `off` of a buffer to 1 KiB of LDS at address dst (one per
 // wave, in M0, which nothing else here uses).  Written out, because the compiler's own
-// form makes every later LDS read wait for it; wait_dma() ends such loads.  There is
-// no destination register that could be reused meanwhile.  The wait states cover a
-// descriptor or address that the vector unit has just put into scalar registers (5).
-__device__ __forceinline__ void dma16(u32x4 b, uint16_t* dst, uint32_t off) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(b)
+// form makes every later LDS read wait for it; wait_loads() ends such loads.  There is
+// no destination register that could be reused meanwhile.
+__device__ __forceinline__ void dma16(u32x4 b, uint32_t dst, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(b)
                  : "memory");
 }
-__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Every load of this wave has ended.  The compiler knows this wait, so it adds none for
+// its own earlier loads after later dma16s, which it would include.
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
 
 // A dense operand, rows of `ld` elements with `cols` summation indices each, that
-// fills tiles by rows.  Base 16-byte aligned, ld and cols multiples of 8, ROWS * ld
-// * 2 bytes under 2^31.
+// fills tiles by rows, step after step.  Base 16-byte aligned, ld and cols multiples
+// of 8, ROWS * ld * 2 bytes under 2^31.
 template <int ROWS, int THREADS>
 struct DenseRows {
-    static constexpr int kLoads = ROWS * 8 / THREADS, kWaveRows = kLoads * 8;
-    const uint16_t* base;
+    static constexpr int kLoads = ROWS * 8 / THREADS;
     static_assert(kLoads % 2 == 0, "8 rows a load: even and odd loads differ in row / 2 & 4");
+    const uint16_t* base;
     uint32_t bytes, off, step;
-    int64_t cols;
+    int64_t left;  // columns from the present step on
     int col, wave;
-    __device__ __forceinline__ DenseRows(const uint16_t* p, int64_t row0, int64_t rows, int64_t ld, int64_t cols_,
+    __device__ __forceinline__ DenseRows(const uint16_t* p, int64_t row0, int64_t rows, int64_t ld, int64_t cols,
                                          int wave_, int lane)
-        : cols(cols_), wave(wave_) {
-        const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
+        : left(cols), wave(wave_) {
+        const int64_t n = rows - row0 < ROWS ? rows - row0 : ROWS;
         base = p + row0 * ld;
-        bytes = (uint32_t)(left * ld * 2);
+        bytes = (uint32_t)(n * ld * 2);
         col = ((lane % 8) ^ (lane / 16)) * 8;
-        off = (uint32_t)((wave * kWaveRows + lane / 8) * ld) * 2;
+        off = (uint32_t)((wave * kLoads * 8 + lane / 8) * ld) * 2;
         step = (uint32_t)(8 * ld * 2);
     }
-    __device__ __forceinline__ void fill(uint16_t* tile, int64_t l0) const {
-        const u32x4 b = buffer(base + l0, bytes);
+    // The present step to the tile at LDS address `tile`; then the next one is present.
+    __device__ __forceinline__ void fill(uint32_t tile) {
+        const u32x4 b = buffer(base, bytes);
+        const int n = left < kDeep ? (int)left : kDeep;  // under 1: none
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int c = i % 2 ? col ^ 32 : col;
-            dma16(b, tile + (wave * kWaveRows + i * 8) * 64, c < cols - l0 ? off + i * step + 2 * c : kOut);
+            dma16(b, tile + (wave * kLoads + i) * 1024, c < n ? off + i * step + 2 * c : kOut);
         }
+        base += kDeep;
+        left -= kDeep;
     }
 };
 
@@ -105,30 +120,46 @@ template <int ROWS, int THREADS>
 struct DenseSteps {
     static constexpr int kChunks = ROWS / 8, kLoads = kDeep * kChunks / THREADS, kLines = 64 / kChunks;
     static_assert(kLines == 2 || kLines == 4, "a wave's 64 chunks are whole lines");
+    static_assert(kLoads % 2 == 0, "even and odd loads differ in l & 2 where a load is 2 lines");
     const uint16_t* base;
-    int64_t lines, ld;
-    uint32_t off[2];  // even and odd loads differ in l & 2 where a load is 2 lines
+    int64_t left;  // lines from the present step on
+    uint32_t line, off[2], step;
     int wave;
-    __device__ __forceinline__ DenseSteps(const uint16_t* p, int64_t col0, int64_t cols, int64_t lines_, int64_t ld_,
+    __device__ __forceinline__ DenseSteps(const uint16_t* p, int64_t col0, int64_t cols, int64_t lines, int64_t ld,
                                           int wave_, int lane)
-        : base(p + col0), lines(lines_), ld(ld_), wave(wave_) {
+        : base(p + col0), left(lines), line((uint32_t)(ld * 2)), wave(wave_) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int l = lane / kChunks + (kLines == 2 ? 2 * h : 0);
+            const int l = lane / kChunks + h * kLines;
             const int c = by_steps_at(lane % kChunks, l) * 8;
-            off[h] = c < cols - col0 ? (uint32_t)((lane / kChunks) * ld + c) * 2 : kOut;
+            off[h] = c < cols - col0 ? (wave * kLoads * kLines + l) * line + 2 * c : kOut;
         }
+        step = 2 * kLines * line;
     }
-    __device__ __forceinline__ void fill(uint16_t* tile, int64_t l0) const {
+    __device__ __forceinline__ void fill(uint32_t tile) {
+        const uint32_t n = left < kDeep ? left > 0 ? (uint32_t)left : 0 : kDeep;
+        const u32x4 b = buffer(base, n * line);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int l = (wave * kLoads + i) * kLines;  // kLoads is even: i & 1 is the parity of l / kLines
-            const int64_t left = lines - l0 - l;
-            const int64_t n = left < 0 ? 0 : left < kLines ? left : kLines;
-            dma16(buffer(base + (l0 + l) * ld, (uint32_t)(n * ld * 2)), tile + l * ROWS, off[i & 1]);
-        }
+        for (int i = 0; i < kLoads; ++i) dma16(b, tile + (wave * kLoads + i) * 1024, off[i % 2] + i / 2 * step);
+        base += (int64_t)line * (kDeep / 2);
+        left -= kDeep;
     }
 };
+
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+// LDS by address.  Kernels short of registers keep one address per tile and derive the
+// others (hidden() stops the compiler from keeping them all across the loop).
+__device__ __forceinline__ bf16x8 lds_read(uint32_t at) { return *(const lds_bf16x8*)(uintptr_t)at; }
+__device__ __forceinline__ void lds_write(uint32_t at, bf16x8 v) { *(lds_bf16x8*)(uintptr_t)at = v; }
+__device__ __forceinline__ uint32_t hidden(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+// address of frag_rows(tile, row, 0, lane) for row a multiple of 32; index s is at
+// this ^ 32 s, rows 32 further at + 4096
+__device__ __forceinline__ uint32_t frag_rows_at(uint32_t tile, int row, int lane) {
+    return tile + 2 * by_rows(row + lane % 32, lane / 32);
+}
 
 // operand registers for v_mfma_f32_32x32x16_bf16: 32 rows from `row`, indices 16 s .. + 15
 __device__ __forceinline__ bf16x8 frag_rows(const uint16_t* tile, int row, int s, int lane) {
@@ -143,6 +174,38 @@ __device__ __forceinline__ bf16x8 frag_steps(uint16_t* tile, int row, int s, int
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + (l + 4) * ROWS + by_steps(c, l) * 8 + h));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
+
+// A tile of BM x COLS outputs on its way through LDS, so that memory sees whole rows.
+template <class S, class T, int COLS>
+struct OutTile {
+    // one pass where the tile fits beside 160 KiB, or a pass for the waves of each tile row
+    static constexpr int kPitch = COLS + 16 / sizeof(T);
+    static constexpr int kPasses = S::BM * kPitch * sizeof(T) > 150000 ? S::WM : 1;
+    static constexpr int kRows = S::BM / kPasses, kSize = kRows * kPitch;
+    // put(tile, pitch): a wave's outputs; row(r): where row r of the tile goes, or null.
+    // Columns j0 .. of rows of `cols`, 16-byte aligned where a row is whole 16-byte pieces.
+    template <class Put, class Row>
+    static __device__ __forceinline__ void store(T* lds, int64_t j0, int64_t cols, Put put, Row row) {
+        constexpr int kVec = 16 / sizeof(T), kWide = COLS / kVec;
+        const bool whole = cols % kVec == 0;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            __syncthreads();
+            if (kPasses == 1 || (int)threadIdx.x / 64 / S::WN == p) put(lds - p * kRows * kPitch, kPitch);
+            __syncthreads();
+            for (int v = threadIdx.x; v < kRows * kWide; v += S::kThreads) {
+                const int r = v / kWide, c = v % kWide * kVec;
+                T* out = row(p * kRows + r);
+                if (!out || j0 + c >= cols) continue;
+                const T* s = lds + r * kPitch + c;
+                if (whole) *reinterpret_cast<u32x4*>(out + j0 + c) = *reinterpret_cast<const u32x4*>(s);
+                else
+                    for (int f = 0; f < kVec; ++f)
+                        if (j0 + c + f < cols) out[j0 + c + f] = s[f];
+            }
+        }
+    }
+};
 
 // Tiles of C in the order that the 8 dies' caches like: workgroup b runs on die
 // b % 8, which gets a run of consecutive tiles, and runs go down bands of `band`

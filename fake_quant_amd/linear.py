@@ -139,6 +139,7 @@ def fql_w4_gated_backward(dh, x, g, u, dtype, m, n, k, group, act, gate, up, dx,
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_CODES = (torch.uint8, torch.int8)
 
 
 def _matrix(nm, what, t, rows=None, cols=None, dtype=None):
@@ -152,33 +153,44 @@ def _matrix(nm, what, t, rows=None, cols=None, dtype=None):
         raise FqError(nm, E_DIM, f"{what} is {tuple(t.shape)}, not {(rows, cols)}")
 
 
-def _triple(nm, what, w, k, group, like):
-    """(codes, scale, zero_point) of a weight dict for rows of k columns, checked."""
+def _weight_dict(nm, what, w, k, group, like):
+    """The C struct of a weight dict for rows of k columns, checked, and the number of rows."""
     if group < 1:
         raise FqError(nm, E_INVALID, f"groups of {group}")
     codes, scale, zp = w["codes"], w["scale"], w.get("zp")
-    if codes.dtype not in (torch.uint8, torch.int8) or scale.dtype != torch.float32 or \
-            (zp is not None and zp.dtype != torch.int32):
+    if codes.dtype not in _CODES or scale.dtype != torch.float32 or (zp is not None and zp.dtype != torch.int32):
         raise FqError(nm, E_UNSUPPORTED, f"{what} needs uint8 codes, float32 scale and int32 zp")
-    n = codes.shape[0]
-    if codes.dim() != 2 or codes.shape[1] != (k + 1) // 2:
-        raise FqError(nm, E_DIM, f"{what} codes are {tuple(codes.shape)}, not 4-bit rows of {k} columns")
-    want = (n, -(-k // group))
-    for part, t in (("scale", scale), ("zp", zp)):
-        if t is not None and tuple(t.shape) != want:
-            raise FqError(nm, E_DIM, f"{what} {part} is {tuple(t.shape)}, not {want}")
-    for part, t in (("codes", codes), ("scale", scale), ("zp", zp)):
-        if t is not None and t.device != like.device:
-            raise FqError(nm, E_INVALID, f"{what} {part} is on {t.device}, not {like.device}")
-    return (codes, scale, zp), n
+    shape = codes.shape
+    if len(shape) != 2 or shape[1] != (k + 1) // 2:
+        raise FqError(nm, E_DIM, f"{what} codes are {tuple(shape)}, not 4-bit rows of {k} columns")
+    want = (shape[0], -(-k // group))
+    if scale.shape != want or (zp is not None and zp.shape != want):
+        raise FqError(nm, E_DIM, f"{what} scale or zp is not {want}")
+    device = like.get_device()
+    if codes.get_device() != device or scale.get_device() != device or (zp is not None and zp.get_device() != device):
+        raise FqError(nm, E_INVALID, f"{what} is not on the device of x")
+    return W4(codes.data_ptr(), scale.data_ptr(), None if zp is None else zp.data_ptr()), shape[0]
 
 
 def _pair(nm, gate, up, k, group, like):
-    wg, n = _triple(nm, "gate", gate, k, group, like)
-    wu, n2 = _triple(nm, "up", up, k, group, like)
+    wg, n = _weight_dict(nm, "gate", gate, k, group, like)
+    wu, n2 = _weight_dict(nm, "up", up, k, group, like)
     if n2 != n:
         raise FqError(nm, E_DIM, f"gate has {n} rows, up {n2}")
     return wg, wu, n
+
+
+def _on_gpu(nm, what, *tensors):
+    for t in tensors:
+        if not t.is_cuda:
+            raise FqError(nm, E_INVALID, f"{what} is not a GPU tensor")
+        if not t.is_contiguous():
+            raise FqError(nm, E_INVALID, f"{what} is not contiguous")
+
+
+def _weight_on_gpu(nm, what, w):
+    zp = w.get("zp")
+    _on_gpu(nm, what, w["codes"], w["scale"], *(() if zp is None else (zp,)))
 
 
 def _act(nm, act):
@@ -187,8 +199,19 @@ def _act(nm, act):
     return ACTS[act]
 
 
+def _chunked(t):
+    """t, or a copy of a view that starts off the 16-byte borders the kernels load from."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _scratch(nbytes, like):
     return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
+# The helpers' checks hold every size, so they call the library without the byte
+# counts of the functions above; a call on one token takes its host about as long
+# as its kernel.  The stream is the current one of x's device.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def w4_matmul(x, w, group):
@@ -196,11 +219,17 @@ def w4_matmul(x, w, group):
     nm = "w4_matmul"
     _matrix(nm, "x", x)
     m, k = x.shape
-    w3, n = _triple(nm, "w", w, k, group, x)
-    dt = _DTYPES[x.dtype]
-    wsb = fql_w4_matmul_workspace_bytes(dt, m, n, k, group)
-    y = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    fql_w4_matmul(x, dt, m, n, k, group, w3, y, _scratch(wsb, x), wsb)
+    ws, n = _weight_dict(nm, "w", w, k, group, x)
+    _on_gpu(nm, "x", x)
+    _weight_on_gpu(nm, "w", w)
+    x, dt = _chunked(x), _DTYPES[x.dtype]
+    y = x.new_empty((m, n))
+    wsb = _lib.fql_w4_matmul_workspace_bytes(dt, m, n, k, group)
+    tmp = _scratch(wsb, x)
+    st = _lib.fql_w4_matmul(x.data_ptr(), dt, m, n, k, group, ctypes.byref(ws), y.data_ptr(), _ptr(tmp), wsb,
+                            _raw_stream(x.get_device()))
+    if st != OK:
+        _check(nm, st)
     return y
 
 
@@ -210,11 +239,19 @@ def w4_gated(x, gate, up, group, act="silu", save=False):
     _matrix(nm, "x", x)
     m, k = x.shape
     wg, wu, n = _pair(nm, gate, up, k, group, x)
-    a, dt = _act(nm, act), _DTYPES[x.dtype]
-    wsb = fql_w4_gated_workspace_bytes(dt, m, n, k, group)
-    h = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    g, u = (torch.empty_like(h), torch.empty_like(h)) if save else (None, None)
-    fql_w4_gated(x, dt, m, n, k, group, a, wg, wu, h, g, u, _scratch(wsb, x), wsb)
+    a = _act(nm, act)
+    _on_gpu(nm, "x", x)
+    _weight_on_gpu(nm, "gate", gate)
+    _weight_on_gpu(nm, "up", up)
+    x, dt = _chunked(x), _DTYPES[x.dtype]
+    h = x.new_empty((m, n))
+    g, u = (x.new_empty((m, n)), x.new_empty((m, n))) if save else (None, None)
+    wsb = _lib.fql_w4_gated_workspace_bytes(dt, m, n, k, group)
+    tmp = _scratch(wsb, x)
+    st = _lib.fql_w4_gated(x.data_ptr(), dt, m, n, k, group, a, ctypes.byref(wg), ctypes.byref(wu), h.data_ptr(), _ptr(g),
+                           _ptr(u), _ptr(tmp), wsb, _raw_stream(x.get_device()))
+    if st != OK:
+        _check(nm, st)
     return (h, g, u) if save else h
 
 
@@ -223,14 +260,22 @@ def w4_matmul_backward(dy, x, w, group, want_dx=True, want_dw=True, dw_dtype=tor
     nm = "w4_matmul_backward"
     _matrix(nm, "x", x)
     m, k = x.shape
-    w3, n = _triple(nm, "w", w, k, group, x)
+    ws, n = _weight_dict(nm, "w", w, k, group, x)
     _matrix(nm, "dy", dy, m, n, x.dtype)
     if dw_dtype not in _DTYPES:
         raise FqError(nm, E_UNSUPPORTED, f"dw_dtype {dw_dtype}, neither float32 nor bfloat16")
-    wsb = fql_w4_matmul_backward_workspace_bytes(m, n, k, group)
+    _on_gpu(nm, "x", x)
+    _on_gpu(nm, "dy", dy)
+    _weight_on_gpu(nm, "w", w)
+    x, dy = _chunked(x), _chunked(dy)
     dx = torch.empty_like(x) if want_dx else None
     dw = torch.empty((n, k), dtype=dw_dtype, device=x.device) if want_dw else None
-    fql_w4_matmul_backward(dy, x, _DTYPES[x.dtype], m, n, k, group, w3, dx, dw, _DTYPES[dw_dtype], _scratch(wsb, x), wsb)
+    wsb = _lib.fql_w4_matmul_backward_workspace_bytes(m, n, k, group)
+    tmp = _scratch(wsb, x)
+    st = _lib.fql_w4_matmul_backward(dy.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], m, n, k, group, ctypes.byref(ws),
+                                     _ptr(dx), _ptr(dw), _DTYPES[dw_dtype], _ptr(tmp), wsb, _raw_stream(x.get_device()))
+    if st != OK:
+        _check(nm, st)
     return dx, dw
 
 
@@ -245,10 +290,19 @@ def w4_gated_backward(dh, x, g, u, gate, up, group, act="silu", want_dx=True, wa
     a = _act(nm, act)
     if dw_dtype not in _DTYPES:
         raise FqError(nm, E_UNSUPPORTED, f"dw_dtype {dw_dtype}, neither float32 nor bfloat16")
-    wsb = fql_w4_gated_backward_workspace_bytes(m, n, k, group)
+    for what, t in (("x", x), ("dh", dh), ("g", g), ("u", u)):
+        _on_gpu(nm, what, t)
+    _weight_on_gpu(nm, "gate", gate)
+    _weight_on_gpu(nm, "up", up)
+    x = _chunked(x)
     dx = torch.empty_like(x) if want_dx else None
     dwg, dwu = ((torch.empty((n, k), dtype=dw_dtype, device=x.device) for _ in range(2)) if want_dw
                 else (None, None))
-    fql_w4_gated_backward(dh, x, g, u, _DTYPES[x.dtype], m, n, k, group, a, wg, wu, dx, dwg, dwu, _DTYPES[dw_dtype],
-                          _scratch(wsb, x), wsb)
+    wsb = _lib.fql_w4_gated_backward_workspace_bytes(m, n, k, group)
+    tmp = _scratch(wsb, x)
+    st = _lib.fql_w4_gated_backward(dh.data_ptr(), x.data_ptr(), g.data_ptr(), u.data_ptr(), _DTYPES[x.dtype], m, n, k,
+                                    group, a, ctypes.byref(wg), ctypes.byref(wu), _ptr(dx), _ptr(dwg), _ptr(dwu),
+                                    _DTYPES[dw_dtype], _ptr(tmp), wsb, _raw_stream(x.get_device()))
+    if st != OK:
+        _check(nm, st)
     return dx, dwg, dwu
