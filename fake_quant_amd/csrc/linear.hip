@@ -140,8 +140,6 @@ bool valid_weight(const fql_w4* w) {
 bool regular(int64_t n, int64_t k, int64_t group) {
     return span_of(group, k) && n * ((k + 1) / 2) >= 16 && k >= 8 && k < kTileWidth;
 }
-bool few_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m <= kFewTokens && regular(n, k, group); }
-bool many_tokens(int64_t m, int64_t n, int64_t k, int64_t group) { return m > kFewTokens && regular(n, k, group); }
 bool tiled_backward(int64_t n, int64_t k, int64_t group) { return regular(n, k, group) && n >= 8 && n < kTileWidth; }
 // Whether a matrix of rows of c elements of 2 bytes is read in place or copied first.
 bool chunked(const void* p, int64_t c) { return c % 8 || fqh::aligned(p, 16); }
@@ -181,10 +179,11 @@ extern "C" {
 
 size_t fql_w4_matmul_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group) {
     if (!fqh::valid_dtype(dtype) || !valid_sizes(m, n, k, group)) return 0;
-    return many_tokens(m, n, k, group) ? forward_workspace(dtype, m, k) : 0;
+    return regular(n, k, group) && !few_tokens(m, n) ? forward_workspace(dtype, m, k) : 0;
 }
 size_t fql_w4_gated_workspace_bytes(int dtype, int64_t m, int64_t n, int64_t k, int64_t group) {
-    return fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
+    if (!fqh::valid_dtype(dtype) || !valid_sizes(m, n, k, group)) return 0;
+    return regular(n, k, group) && !few_tokens(m, 2 * n) ? forward_workspace(dtype, m, k) : 0;
 }
 size_t fql_w4_matmul_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int64_t group) {
     return valid_sizes(m, n, k, group) && tiled_backward(n, k, group) ? backward_workspace(m, n, k, false) : 0;
@@ -201,8 +200,8 @@ int fql_w4_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int
     if (!x || !y || !fqh::aligned(x, elem(dtype)) || !fqh::aligned(y, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_matmul_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
-    if (few_tokens(m, n, k, group)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
-    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(y, n, elem(dtype)))
+    if (regular(n, k, group) && few_tokens(m, n)) return few_matmul(x, dtype, m, n, k, group, *w, y, stream);
+    if (regular(n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(y, n, elem(dtype)))
         return forward_matmul(x, dtype, m, n, k, group, *w, y, workspace, stream);
     return dtype == FQ_F32 ? matmul<float>(x, m, n, k, group, *w, y, stream)
                            : matmul<uint16_t>(x, m, n, k, group, *w, y, stream);
@@ -219,8 +218,9 @@ int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int6
         if (!fqh::aligned(p, elem(dtype))) return FQ_E_INVALID;
     const size_t need = fql_w4_gated_workspace_bytes(dtype, m, n, k, group);
     if (need && (!workspace || workspace_bytes < need || !fqh::aligned(workspace, 16))) return FQ_E_INVALID;
-    if (few_tokens(m, n, k, group)) return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
-    if (many_tokens(m, n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(h, n, elem(dtype)) &&
+    if (regular(n, k, group) && few_tokens(m, 2 * n))
+        return few_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, stream);
+    if (regular(n, k, group) && (need || fqh::aligned(x, 16)) && stored_whole(h, n, elem(dtype)) &&
         stored_whole(g, n, elem(dtype)) && stored_whole(u, n, elem(dtype)))
         return forward_gated(x, dtype, m, n, k, group, act, *gate, *up, h, g, u, workspace, stream);
     return dtype == FQ_F32 ? gated<float>(x, m, n, k, group, act, *gate, *up, h, g, u, stream)

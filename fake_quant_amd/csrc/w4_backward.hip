@@ -17,9 +17,9 @@ struct DxArgs {
     const uint16_t* dy;  // [m] rows, ld apart, of `cols` columns: n, or two runs of `run` >= n for a pair of weights
     int64_t ld, cols, run;
     W4Mat w[2];
-    uint16_t* dx;
+    void* dx;
     int64_t m, n, k;
-    uint32_t ni, nj;
+    uint32_t ni, nj, steps;  // steps: of one workgroup, an even number where the sum is split
     // one weight of a pair may have no zero-points: then any readable words, masked to zeros
     const int32_t* zp[2];
     int32_t mask[2];
@@ -31,7 +31,7 @@ struct DwArgs {
     int64_t ld, cols, run, ldx;
     T* dw[2];
     int64_t m, n, k;
-    uint32_t ni, nj;
+    uint32_t ni, nj, steps;
 };
 
 // The weights' side of a tile, 64 rows by BN columns: a thread holds 32 codes of a row.
@@ -45,9 +45,10 @@ template <int BN, bool ZP>
 struct CodeSteps {
     static constexpr int kParts = BN / 32, kLoads = ZP ? 3 : 2;
     const DxArgs& a;
-    int64_t byte, gi, l0 = 0;
+    int64_t byte, gi, l0;
     int line, part;
-    __device__ __forceinline__ CodeSteps(const DxArgs& a_, int64_t col0, int t) : a(a_), line(t / kParts), part(t % kParts) {
+    __device__ __forceinline__ CodeSteps(const DxArgs& a_, int64_t col0, int64_t l0_, int t)
+        : a(a_), l0(l0_), line(t / kParts), part(t % kParts) {
         const int64_t col = col0 + 32 * part;
         byte = col / 2;
         gi = (col < a.k ? col : a.k - 1) / a.w[0].group;
@@ -68,7 +69,7 @@ struct CodeSteps {
         d.c = load16(a.w[which].codes + at * a.w[0].row_bytes + (left < 16 ? byte + left - 16 : byte));
         d.s = a.w[which].scale[at * a.w[0].ng + gi];
         if constexpr (ZP) d.z = a.zp[which][at * a.w[0].ng + gi], d.mask = a.mask[which];
-        d.none = r >= a.n;
+        d.none = r >= a.n || l0 >= a.cols;
         l0 += kDeep;
     }
     // Puts in place what the last load() read.
@@ -126,17 +127,19 @@ struct TileLds {
 
 // RAGGED: k is no multiple of 32, so that a thread's run of codes may end inside the
 // matrix (a branch that costs the others 30%: 177 against 135 us at 4096^3).
-template <class S, bool ZP, bool RAGGED>
+// T: bfloat16 for dx itself; float for partial sums, one [m, k] matrix per blockIdx.y.
+template <class S, bool ZP, bool RAGGED, class T>
 __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
-    __shared__ TileLds<S, uint16_t> lds;
+    __shared__ TileLds<S, T> lds;
     const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
     uint32_t ti, tj;
     tile_at(blockIdx.x, a.ni, a.nj, ti, tj);
     const int64_t i0 = (int64_t)ti * S::BM, j0 = (int64_t)tj * S::BN;
-    DenseRows<S::BM, S::kThreads> ys(a.dy, i0, a.m, a.ld, a.cols, wave, lane);
-    CodeSteps<S::BN, ZP> ws(a, j0, t);
+    const int64_t l0 = (int64_t)blockIdx.y * a.steps * kDeep;
+    DenseRows<S::BM, S::kThreads> ys(a.dy + l0, i0, a.m, a.ld, a.cols - l0, wave, lane);
+    CodeSteps<S::BN, ZP> ws(a, j0, l0, t);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
-    const uint32_t steps = (uint32_t)((a.cols + kDeep - 1) / kDeep);
+    T* const dx = (T*)a.dx + blockIdx.y * a.m * a.k;
 
     f32x16 acc[S::MS][S::NS] = {};
     Frags<S> f[2];
@@ -184,12 +187,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     read(f[0], 0, 0);
     ws.template store<0>(lds.b[1], c);
     ws.template store<1>(lds.b[1], c);
-    for (uint32_t st = 0; st < steps; ++st) stage(st & 1);
+    for (uint32_t st = 0; st < a.steps; ++st) stage(st & 1);  // past the end both operands are zeros
     wait_loads();
-    __syncthreads();
-    OutTile<S, uint16_t, S::BN>::store(
-        lds.out, j0, a.k, [&](uint16_t* out, int pitch) { put_sums<S>(acc, out, pitch); },
-        [&](int r) { return i0 + r < a.m ? a.dx + (i0 + r) * a.k : nullptr; });
+    OutTile<S, T, S::BN>::store(
+        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch); },
+        [&](int r) { return i0 + r < a.m ? dx + (i0 + r) * a.k : nullptr; });
 }
 
 template <class S, class T>
@@ -199,10 +201,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
     uint32_t ti, tj;
     tile_at(blockIdx.x, a.ni, a.nj, ti, tj);
     const int64_t i0 = (int64_t)ti * S::BM, j0 = (int64_t)tj * S::BN;
-    DenseSteps<S::BM, S::kThreads> ys(a.dy, i0, a.cols, a.m, a.ld, wave, lane);
-    DenseSteps<S::BN, S::kThreads> xs(a.x, j0, a.ldx, a.m, a.ldx, wave, lane);
+    const int64_t l0 = (int64_t)blockIdx.y * a.steps * kDeep;
+    DenseSteps<S::BM, S::kThreads> ys(a.dy + l0 * a.ld, i0, a.cols, a.m - l0, a.ld, wave, lane);
+    DenseSteps<S::BN, S::kThreads> xs(a.x + l0 * a.ldx, j0, a.ldx, a.m - l0, a.ldx, wave, lane);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
-    const uint32_t steps = (uint32_t)((a.m + kDeep - 1) / kDeep);
+    T* const part = a.dw[0] + blockIdx.y * a.cols * a.k;  // blockIdx.y > 0: partial sums only
 
     f32x16 acc[S::MS][S::NS] = {};
     Frags<S> f[2];
@@ -234,17 +237,16 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
         read(f[0], cur ^ 1, 0);
         multiply<S>(acc, f[1]);
     };
-    for (uint32_t st = 0; st < steps; st += 2) {  // past the end both operands are zeros
+    for (uint32_t st = 0; st < a.steps; st += 2) {  // past the end both operands are zeros
         stage(0);
         stage(1);
     }
     wait_loads();
-    __syncthreads();
     OutTile<S, T, S::BN>::store(
         lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch); },
         [&](int r) -> T* {
             const int64_t i = i0 + r, f = i < a.run ? i : i - a.run;
-            return i < a.cols && f < a.n ? a.dw[i < a.run ? 0 : 1] + f * a.k : nullptr;
+            return i < a.cols && f < a.n ? (i < a.run ? part : a.dw[1]) + f * a.k : nullptr;
         });
 }
 
@@ -295,63 +297,123 @@ const uint16_t* chunk_rows(const void* p, int64_t rows, int64_t cols, char*& at,
     return out;
 }
 
-template <class S>
-int launch_dx(DxArgs a, bool zp, hipStream_t stream) {
-    const int64_t ni = (a.m + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
+// The sum of `splits` matrices of `rows` rows of k, rows run .. of it in out2.
+template <class T>
+__global__ __launch_bounds__(256) void k_join(const float* part, int splits, int64_t rows, int64_t n, int64_t run,
+                                              int64_t k, T* out, T* out2) {
+    const int64_t all = rows * k;
+    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < all; v += gridDim.x * 256ll) {
+        const int64_t i = v / k, f = i < run ? i : i - run;
+        if (f >= n) continue;
+        float sum = part[v];
+        for (int p = 1; p < splits; ++p) sum += part[p * all + v];
+        store_f((i < run ? out : out2) + f * k + v % k, sum);
+    }
+}
+
+using Big = Shape<256, 256, 2, 4>;
+using Mid = Shape<128, 256, 2, 4>;
+
+// How a product of rows x cols outputs over `deep` indices is cut.
+struct Cut {
+    bool big;
+    uint32_t steps, splits;
+};
+Cut cut(int64_t rows, int64_t cols, int64_t deep) {
+    const bool big = big_tiles(rows, cols);
+    const int64_t all = (deep + kDeep - 1) / kDeep, mid = ((rows + 127) / 128) * ((cols + 255) / 256);
+    // A few tiles leave most compute units idle: their sums are split into pieces of
+    // four steps or more until the units are busy, and joined by a second kernel.
+    int64_t splits = big || mid > kUnits / 2 ? 1 : kUnits / mid < all / 4 ? kUnits / mid : all / 4;
+    if (splits < 2) return {big, (uint32_t)all, 1};
+    const int64_t steps = ((all + splits - 1) / splits + 1) / 2 * 2;
+    return {false, (uint32_t)steps, (uint32_t)((all + steps - 1) / steps)};
+}
+size_t cut_bytes(int64_t rows, int64_t cols, int64_t deep) {
+    const Cut c = cut(rows, cols, deep);
+    return c.splits > 1 ? (size_t)(c.splits * rows * cols * 4 + 15) / 16 * 16 : 0;
+}
+
+template <class S, class T>
+void launch_dx(const DxArgs& a, dim3 g, hipStream_t stream) {
+    const bool zp = a.w[0].zp || a.w[1].zp;
+    if (a.k % 32) zp ? k_dx<S, true, true, T><<<g, S::kThreads, 0, stream>>>(a) : k_dx<S, false, true, T><<<g, S::kThreads, 0, stream>>>(a);
+    else zp ? k_dx<S, true, false, T><<<g, S::kThreads, 0, stream>>>(a) : k_dx<S, false, false, T><<<g, S::kThreads, 0, stream>>>(a);
+}
+
+int input_gradient(DxArgs a, float* part, hipStream_t stream) {
+    const Cut c = cut(a.m, a.k, a.cols);
+    const int64_t ni = (a.m + (c.big ? 255 : 127)) / (c.big ? 256 : 128), nj = (a.k + 255) / 256;
     if (ni * nj > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
-    a.ni = (uint32_t)ni, a.nj = (uint32_t)nj;
+    a.ni = (uint32_t)ni, a.nj = (uint32_t)nj, a.steps = c.steps;
     for (int i = 0; i < 2; ++i) {
         a.zp[i] = a.w[i].zp ? a.w[i].zp : reinterpret_cast<const int32_t*>(a.w[i].scale);
         a.mask[i] = a.w[i].zp ? -1 : 0;
     }
-    const dim3 g((unsigned)(ni * nj)), b(S::kThreads);
-    if (a.k % 32) zp ? k_dx<S, true, true><<<g, b, 0, stream>>>(a) : k_dx<S, false, true><<<g, b, 0, stream>>>(a);
-    else zp ? k_dx<S, true, false><<<g, b, 0, stream>>>(a) : k_dx<S, false, false><<<g, b, 0, stream>>>(a);
+    const dim3 g((unsigned)(ni * nj), c.splits);
+    if (c.big) {
+        launch_dx<Big, uint16_t>(a, g, stream);
+    } else if (c.splits == 1) {
+        launch_dx<Mid, uint16_t>(a, g, stream);
+    } else {
+        uint16_t* dx = (uint16_t*)a.dx;
+        a.dx = part;
+        launch_dx<Mid, float>(a, g, stream);
+        k_join<<<fqh::grid_all(a.m * a.k, 256), 256, 0, stream>>>(part, (int)c.splits, a.m, a.m, a.m, a.k, dx, dx);
+    }
     return fqh::launched();
 }
-template <class S, class T>
-int launch_dw(DwArgs<T> a, hipStream_t stream) {
-    const int64_t ni = (a.cols + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
+
+template <class T>
+int weight_gradient(DwArgs<T> a, float* part, hipStream_t stream) {
+    const Cut c = cut(a.cols, a.k, a.m);
+    const int64_t ni = (a.cols + (c.big ? 255 : 127)) / (c.big ? 256 : 128), nj = (a.k + 255) / 256;
     if (ni * nj > 0x7FFFFFFF) return FQ_E_UNSUPPORTED;
-    a.ni = (uint32_t)ni, a.nj = (uint32_t)nj;
-    k_dw<S, T><<<dim3((unsigned)(ni * nj)), dim3(S::kThreads), 0, stream>>>(a);
+    a.ni = (uint32_t)ni, a.nj = (uint32_t)nj, a.steps = c.steps;
+    const dim3 g((unsigned)(ni * nj), c.splits);
+    if (c.big) {
+        k_dw<Big, T><<<g, Big::kThreads, 0, stream>>>(a);
+    } else if (c.splits == 1) {
+        k_dw<Mid, T><<<g, Mid::kThreads, 0, stream>>>(a);
+    } else {
+        const DwArgs<float> p{a.dy, a.x, a.ld, a.cols, a.cols, a.ldx, {part, part}, a.m, a.cols, a.k, a.ni, a.nj, a.steps};
+        k_dw<Mid, float><<<g, Mid::kThreads, 0, stream>>>(p);
+        k_join<<<fqh::grid_all(a.cols * a.k, 256), 256, 0, stream>>>(part, (int)c.splits, a.cols, a.n, a.run, a.k, a.dw[0], a.dw[1]);
+    }
     return fqh::launched();
 }
 
-using Big = Shape<256, 256, 2, 4>;
-using Small = Shape<128, 128, 2, 2>;
-bool big_tiles(int64_t rows, int64_t cols) { return ((rows + 255) / 256) * ((cols + 255) / 256) >= fqh::num_cus() / 2; }
-
-int products(const DxArgs& dx, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype, hipStream_t stream) {
+int products(const DxArgs& dx, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype, void* part,
+             hipStream_t stream) {
     if (dx.dx) {
-        const bool zp = dx.w[0].zp || dx.w[1].zp;
-        const int st = big_tiles(dx.m, dx.k) ? launch_dx<Big>(dx, zp, stream) : launch_dx<Small>(dx, zp, stream);
+        const int st = input_gradient(dx, (float*)part, stream);
         if (st != FQ_OK || !dw) return st;
     }
-    const bool big = big_tiles(dx.cols, dx.k);
-    if (dw_dtype == FQ_F32) {
-        const DwArgs<float> a{dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(float*)dw, (float*)dw2}, dx.m, dx.n, dx.k};
-        return big ? launch_dw<Big>(a, stream) : launch_dw<Small>(a, stream);
-    }
-    const DwArgs<uint16_t> a{dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(uint16_t*)dw, (uint16_t*)dw2}, dx.m, dx.n, dx.k};
-    return big ? launch_dw<Big>(a, stream) : launch_dw<Small>(a, stream);
+    if (dw_dtype == FQ_F32)
+        return weight_gradient<float>({dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(float*)dw, (float*)dw2}, dx.m, dx.n, dx.k},
+                                      (float*)part, stream);
+    return weight_gradient<uint16_t>(
+        {dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(uint16_t*)dw, (uint16_t*)dw2}, dx.m, dx.n, dx.k}, (float*)part, stream);
 }
 
 }  // namespace
 
 size_t backward_workspace(int64_t m, int64_t n, int64_t k, bool gated) {
-    const int64_t a = gated ? 2 * padded(n, kDeep) : n % 8 ? padded(n, 8) : 0, b = k % 8 ? padded(k, 8) : 0;
-    return (size_t)(m * (a + b) * 2);
+    const int64_t cols = gated ? 2 * padded(n, kDeep) : padded(n, 8);
+    const int64_t a = gated || n % 8 ? cols : 0, b = k % 8 ? padded(k, 8) : 0;
+    const size_t dx = cut_bytes(m, k, cols), dw = cut_bytes(cols, k, m);  // one after the other
+    return (size_t)(m * (a + b) * 2) + (dx > dw ? dx : dw);
 }
 
 int matmul_backward(const void* dy, const void* x, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4* w,
                     void* dx, void* dw, int dw_dtype, void* workspace, hipStream_t stream) {
     char* at = (char*)workspace;
     const uint16_t* y = chunk_rows(dy, m, n, at, stream);
+    const uint16_t* xs = dw ? chunk_rows(x, m, k, at, stream) : nullptr;
     const W4Mat wm = dx ? w4_mat(*w, k, group) : W4Mat{};
     const int64_t ld = padded(n, 8);
-    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, (uint16_t*)dx, m, n, k},
-                    dw ? chunk_rows(x, m, k, at, stream) : nullptr, padded(k, 8), dw, nullptr, dw_dtype, stream);
+    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, dx, m, n, k}, xs, padded(k, 8), dw, nullptr, dw_dtype, at,
+                    stream);
 }
 
 int gated_backward(const void* dh, const void* x, const void* g, const void* u, int64_t m, int64_t n, int64_t k,
@@ -362,10 +424,10 @@ int gated_backward(const void* dh, const void* x, const void* g, const void* u, 
     char* at = (char*)(both + m * 2 * run);
     k_gate_grad<<<fqh::grid_all(m * run / 8, 256), 256, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g,
                                                                      (const uint16_t*)u, act, m, n, run, both);
-    DxArgs a{both, 2 * run, 2 * run, run, {}, (uint16_t*)dx, m, n, k};
+    const uint16_t* xs = dw_gate ? chunk_rows(x, m, k, at, stream) : nullptr;
+    DxArgs a{both, 2 * run, 2 * run, run, {}, dx, m, n, k};
     if (dx) a.w[0] = w4_mat(*gate, k, group), a.w[1] = w4_mat(*up, k, group);
-    return products(a, dw_gate ? chunk_rows(x, m, k, at, stream) : nullptr, padded(k, 8), dw_gate, dw_up, dw_dtype,
-                    stream);
+    return products(a, xs, padded(k, 8), dw_gate, dw_up, dw_dtype, at, stream);
 }
 
 }  // namespace fqw

@@ -259,12 +259,9 @@ int forward(ForwardArgs<T> a, const T* x, int64_t group, void* workspace, hipStr
         a.mask[i] = a.w[i].zp ? -1 : 0;
     }
     using Big = Shape<256, 256, 2, 4>;
-    using Small = Shape<128, 128, 2, 2>;
-    const int64_t big = ((a.m + 255) / 256) * ((a.n * W + 255) / 256);
-    if (big >= fqh::num_cus() / 2) {
-        return fine ? launch<Big, 32, W, T>(a, zp, stream) : launch<Big, 64, W, T>(a, zp, stream);
-    }
-    return fine ? launch<Small, 32, W, T>(a, zp, stream) : launch<Small, 64, W, T>(a, zp, stream);
+    using Mid = Shape<128, 256, 2, 4>;
+    if (big_tiles(a.m, a.n * W)) return fine ? launch<Big, 32, W, T>(a, zp, stream) : launch<Big, 64, W, T>(a, zp, stream);
+    return fine ? launch<Mid, 32, W, T>(a, zp, stream) : launch<Mid, 64, W, T>(a, zp, stream);
 }
 
 }  // namespace
