@@ -3,9 +3,10 @@
 // other, so that one pair of products serves both matrices.
 //
 // What bounds it: the matrix instructions.  dx sums over the rows of W, whose
-// scales differ, so W enters as bfloat16 rounded to nearest (2^-8 of a value at
-// most, as bfloat16 gradients themselves); dw holds no weight and its products are
-// exact.  dg and du are rounded to bfloat16 for the same instructions.
+// scales differ, so W enters rounded: to bfloat16 (2^-8 of a value at most, no more
+// than a bfloat16 dx itself) beside a bfloat16 dy, to half precision (2^-11) beside dg
+// and du, which are rounded too.  dw holds no weight; its products are exact, but for
+// dg and du rounded to bfloat16.
 #include "fq_host.h"
 #include "w4_linear.h"
 #include "w4_tile.h"
@@ -20,6 +21,9 @@ struct DxArgs {
     void* dx;
     int64_t m, n, k;
     uint32_t ni, nj, steps;  // steps: of one workgroup, an even number where the sum is split
+    // dy in half precision: column c of row r times 2^(shift[r]) / down[c]
+    const int32_t* shift;
+    const float* down;
     // one weight of a pair may have no zero-points: then any readable words, masked to zeros
     const int32_t* zp[2];
     int32_t mask[2];
@@ -37,11 +41,11 @@ struct DwArgs {
 // The weights' side of a tile, 64 rows by BN columns: a thread holds 32 codes of a row.
 struct CodeRegs {
     u32x4 c;
-    float s;
+    float s, down;
     int32_t z, mask;
     bool none;
 };
-template <int BN, bool ZP>
+template <int BN, bool ZP, bool HALF>
 struct CodeSteps {
     static constexpr int kParts = BN / 32, kLoads = ZP ? 3 : 2;
     const DxArgs& a;
@@ -68,6 +72,7 @@ struct CodeSteps {
         // past the matrix a thread reads its last 16 bytes, which whole() puts in place
         d.c = load16(a.w[which].codes + at * a.w[0].row_bytes + (left < 16 ? byte + left - 16 : byte));
         d.s = a.w[which].scale[at * a.w[0].ng + gi];
+        if constexpr (HALF) d.down = a.down[(which ? a.run : 0) + at];
         if constexpr (ZP) d.z = a.zp[which][at * a.w[0].ng + gi], d.mask = a.mask[which];
         d.none = r >= a.n || l0 >= a.cols;
         l0 += kDeep;
@@ -81,30 +86,38 @@ struct CodeSteps {
     // Codes 8 J .. of those to a tile.
     template <int J>
     __device__ __forceinline__ void store(uint16_t* tile, const CodeRegs& d) const {
+        const float z = ZP ? (float)(d.z & d.mask) * 0.0625f : 0.0f, s = d.none ? 0.0f : d.s * 16.0f;
         *reinterpret_cast<bf16x8*>(tile + line * BN + by_steps(4 * part + J, line) * 8) =
-            weights_bf16<ZP>(d.c[J], ZP ? (float)(d.z & d.mask) * 0.0625f : 0.0f, d.none ? 0.0f : d.s * 16.0f);
+            HALF ? weights_half<ZP>(d.c[J], z, s * d.down) : weights_bf16<ZP>(d.c[J], z, s);
     }
 };
 
-// A wave's sums to its rows and columns of a tile in LDS: lanes hold one row each and runs of four columns.
-template <class S, class T>
-__device__ __forceinline__ void put_sums(const f32x16 (&acc)[S::MS][S::NS], T* lds, int pitch) {
+// A wave's sums to its rows and columns of a tile in LDS: lanes hold one row each and
+// runs of four columns.  exponent(row) halves a row's sums that often.
+template <class S, class T, class Exponent>
+__device__ __forceinline__ void put_sums(const f32x16 (&acc)[S::MS][S::NS], T* lds, int pitch, Exponent exponent) {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     T* at = lds + (wave / S::WN * (S::MS * 32) + lane % 32) * pitch + wave % S::WN * (S::NS * 32) + 4 * (lane / 32);
 #pragma unroll
-    for (int i = 0; i < S::MS; ++i)
+    for (int i = 0; i < S::MS; ++i) {
+        const int down = exponent(wave / S::WN * (S::MS * 32) + 32 * i + lane % 32);
 #pragma unroll
         for (int j = 0; j < S::NS; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) store_f(at + 32 * i * pitch + 32 * j + e / 4 * 8 + e % 4, acc[i][j][e]);
+            for (int e = 0; e < 16; ++e)
+                store_f(at + 32 * i * pitch + 32 * j + e / 4 * 8 + e % 4, __builtin_amdgcn_ldexpf(acc[i][j][e], -down));
+    }
 }
+struct NoExponent {
+    __device__ __forceinline__ int operator()(int) const { return 0; }
+};
 
 // Operand registers of half a step, and their products.
 template <class S>
 struct Frags {
     bf16x8 a[S::MS][2], b[S::NS][2];
 };
-template <class S>
+template <class S, bool HALF = false>
 __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MS][S::NS], const Frags<S>& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -112,7 +125,11 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MS][S::NS], const Frag
         for (int i = 0; i < S::MS; ++i)
 #pragma unroll
             for (int j = 0; j < S::NS; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
+                if constexpr (HALF)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, f.b[j][h]),
+                                                                       __builtin_bit_cast(f16x8, f.a[i][h]), acc[i][j], 0, 0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
 }
 
 template <class S, class T>
@@ -128,7 +145,7 @@ struct TileLds {
 // RAGGED: k is no multiple of 32, so that a thread's run of codes may end inside the
 // matrix (a branch that costs the others 30%: 177 against 135 us at 4096^3).
 // T: bfloat16 for dx itself; float for partial sums, one [m, k] matrix per blockIdx.y.
-template <class S, bool ZP, bool RAGGED, class T>
+template <class S, bool ZP, bool RAGGED, bool HALF, class T>
 __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     __shared__ TileLds<S, T> lds;
     const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
@@ -137,7 +154,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     const int64_t i0 = (int64_t)ti * S::BM, j0 = (int64_t)tj * S::BN;
     const int64_t l0 = (int64_t)blockIdx.y * a.steps * kDeep;
     DenseRows<S::BM, S::kThreads> ys(a.dy + l0, i0, a.m, a.ld, a.cols - l0, wave, lane);
-    CodeSteps<S::BN, ZP> ws(a, j0, l0, t);
+    CodeSteps<S::BN, ZP, HALF> ws(a, j0, l0, t);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
     T* const dx = (T*)a.dx + blockIdx.y * a.m * a.k;
 
@@ -160,7 +177,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
         read(f[1], cur, 1);
         ws.template store<2>(lds.b[cur ^ 1], c);
         ws.template store<3>(lds.b[cur ^ 1], c);
-        multiply<S>(acc, f[0]);
+        multiply<S, HALF>(acc, f[0]);
         wait_loads();
         if constexpr (RAGGED) ws.whole(ahead);
         __syncthreads();  // the other stage is full, and this one has been read
@@ -169,7 +186,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
         read(f[0], cur ^ 1, 0);
         ws.template store<0>(lds.b[cur], c);
         ws.template store<1>(lds.b[cur], c);
-        multiply<S>(acc, f[1]);
+        multiply<S, HALF>(acc, f[1]);
     };
     ws.load(c);
     if constexpr (RAGGED) ws.whole(c);
@@ -190,7 +207,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     for (uint32_t st = 0; st < a.steps; ++st) stage(st & 1);  // past the end both operands are zeros
     wait_loads();
     OutTile<S, T, S::BN>::store(
-        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch); },
+        lds.out, j0, a.k, [&](T* out, int pitch) {
+            if constexpr (HALF) put_sums<S>(acc, out, pitch, [&](int r) { return i0 + r < a.m ? a.shift[i0 + r] : 0; });
+            else put_sums<S>(acc, out, pitch, NoExponent{});
+        },
         [&](int r) { return i0 + r < a.m ? dx + (i0 + r) * a.k : nullptr; });
 }
 
@@ -243,33 +263,107 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
     }
     wait_loads();
     OutTile<S, T, S::BN>::store(
-        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch); },
+        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch, NoExponent{}); },
         [&](int r) -> T* {
             const int64_t i = i0 + r, f = i < a.run ? i : i - a.run;
             return i < a.cols && f < a.n ? (i < a.run ? part : a.dw[1]) + f * a.k : nullptr;
         });
 }
 
-// dg and du beside each other: out [m][2 run], zeros in columns n .. run - 1 of each half.
-__global__ __launch_bounds__(256) void k_gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
-                                                   int64_t m, int64_t n, int64_t run, uint16_t* out) {
-    const int64_t chunks = run / 8;
-    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < m * chunks; v += gridDim.x * 256ll) {
-        const int64_t r = v / chunks, c = v % chunks * 8, at = r * n + c;
-        Tokens<uint16_t> td, tg, tu;
-        td.load_part(dh + at, n - c), tg.load_part(g + at, n - c), tu.load_part(u + at, n - c);
-        bf16x8 d[1], gg[1], uu[1], dg, du;
-        td.parts(d), tg.parts(gg), tu.parts(uu);
+// dg and du of eight columns from c on, zeros past the row's end.
+__device__ __forceinline__ void gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act, int64_t left,
+                                          float (&dg)[8], float (&du)[8]) {
+    Tokens<uint16_t> td, tg, tu;
+    td.load_part(dh, left), tg.load_part(g, left), tu.load_part(u, left);
+    bf16x8 d[1], gg[1], uu[1];
+    td.parts(d), tg.parts(gg), tu.parts(uu);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float value, slope;
-            const float di = (float)d[0][i];
-            act_both(act, (float)gg[0][i], value, slope);
-            dg[i] = (__bf16)(di * (float)uu[0][i] * slope);
-            du[i] = (__bf16)(di * value);
+    for (int i = 0; i < 8; ++i) {
+        const float di = (float)d[0][i];
+        float value, slope;
+        act_both(act, (float)gg[0][i], value, slope);
+        dg[i] = di * (float)uu[0][i] * slope;
+        du[i] = di * value;
+    }
+}
+
+// dg and du beside each other, [m][2 run], zeros in columns n .. run - 1 of each half.
+//
+// For dw in bfloat16.  For dx in half precision, whose 11 bits (and the weights' there)
+// leave the sums as good as rounded once; bfloat16 on both sides would have added two
+// roundings of 2^-8 to that of dx.  Half precision spans little range, so each row of
+// a weight is divided by the power of two of its largest scale, dg and du are
+// multiplied by it, and each token is multiplied by 2^shift, which puts its largest
+// magnitude at 2^12 .. 2^13: what that loses lies 2^-37 under a token's largest value.
+// One workgroup per token forms the values twice, for the largest and to write them.
+__global__ __launch_bounds__(256) void k_gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
+                                                   int64_t n, int64_t run, const float* up, uint16_t* half,
+                                                   int32_t* shift, uint16_t* out) {
+    __shared__ float wave_max[4];
+    const int64_t r = blockIdx.x, at = r * n;
+    int sh = 0;
+    if (half) {
+        float top = 0.0f;
+        for (int64_t c = threadIdx.x * 8; c < n; c += 2048) {
+            float dg[8], du[8];
+            gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, dg, du);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = fabsf(dg[i] * up[c + i]), b = fabsf(du[i] * up[run + c + i]);
+                if (a < INFINITY) top = fmaxf(top, a);
+                if (b < INFINITY) top = fmaxf(top, b);
+            }
         }
-        *reinterpret_cast<bf16x8*>(out + r * 2 * run + c) = dg;
-        *reinterpret_cast<bf16x8*>(out + r * 2 * run + run + c) = du;
+#pragma unroll
+        for (int o = 32; o; o /= 2) top = fmaxf(top, __shfl_xor(top, o));
+        if (threadIdx.x % 64 == 0) wave_max[threadIdx.x / 64] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+        if (top > 0.0f) sh = 13 - __builtin_amdgcn_frexp_expf(top);
+        if (threadIdx.x == 0) shift[r] = sh;
+    }
+    for (int64_t c = threadIdx.x * 8; c < run; c += 2048) {
+        float dg[8], du[8];
+        gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, dg, du);
+        if (out) {
+            bf16x8 a, b;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = (__bf16)dg[i], b[i] = (__bf16)du[i];
+            *reinterpret_cast<bf16x8*>(out + r * 2 * run + c) = a;
+            *reinterpret_cast<bf16x8*>(out + r * 2 * run + run + c) = b;
+        }
+        if (half) {
+            f16x8 a, b;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                a[i] = (_Float16)__builtin_amdgcn_ldexpf(dg[i] * up[c + i], sh);
+                b[i] = (_Float16)__builtin_amdgcn_ldexpf(du[i] * up[run + c + i], sh);
+            }
+            *reinterpret_cast<f16x8*>(half + r * 2 * run + c) = a;
+            *reinterpret_cast<f16x8*>(half + r * 2 * run + run + c) = b;
+        }
+    }
+}
+
+// up[i]: the power of two of the largest finite scale of row i of two weights, one
+// below the other in `run` rows each (1 where there is none); down[i] = 1 / up[i].
+// 16 lanes a row.
+__global__ __launch_bounds__(256) void k_row_powers(const float* gate, const float* below, int64_t n, int64_t run,
+                                                    int64_t ng, float* up, float* down) {
+    const int64_t i = blockIdx.x * 16ll + threadIdx.x / 16, r = i < run ? i : i - run;
+    if (i >= 2 * run) return;
+    float top = 0.0f;
+    for (int64_t c = threadIdx.x % 16; r < n && c < ng; c += 16) {
+        const float s = fabsf((i < run ? gate : below)[r * ng + c]);
+        if (s < INFINITY) top = fmaxf(top, s);
+    }
+#pragma unroll
+    for (int o = 8; o; o /= 2) top = fmaxf(top, __shfl_xor(top, o, 16));
+    int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
+    e = e < -120 ? -120 : e > 120 ? 120 : e;
+    if (threadIdx.x % 16 == 0) {
+        up[i] = __builtin_amdgcn_ldexpf(1.0f, e);
+        down[i] = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
 }
 
@@ -334,11 +428,16 @@ size_t cut_bytes(int64_t rows, int64_t cols, int64_t deep) {
     return c.splits > 1 ? (size_t)(c.splits * rows * cols * 4 + 15) / 16 * 16 : 0;
 }
 
+template <class S, bool HALF, class T>
+void launch_dx_as(const DxArgs& a, dim3 g, hipStream_t stream) {
+    const bool zp = a.w[0].zp || a.w[1].zp;
+    const dim3 b(S::kThreads);
+    if (a.k % 32) zp ? k_dx<S, true, true, HALF, T><<<g, b, 0, stream>>>(a) : k_dx<S, false, true, HALF, T><<<g, b, 0, stream>>>(a);
+    else zp ? k_dx<S, true, false, HALF, T><<<g, b, 0, stream>>>(a) : k_dx<S, false, false, HALF, T><<<g, b, 0, stream>>>(a);
+}
 template <class S, class T>
 void launch_dx(const DxArgs& a, dim3 g, hipStream_t stream) {
-    const bool zp = a.w[0].zp || a.w[1].zp;
-    if (a.k % 32) zp ? k_dx<S, true, true, T><<<g, S::kThreads, 0, stream>>>(a) : k_dx<S, false, true, T><<<g, S::kThreads, 0, stream>>>(a);
-    else zp ? k_dx<S, true, false, T><<<g, S::kThreads, 0, stream>>>(a) : k_dx<S, false, false, T><<<g, S::kThreads, 0, stream>>>(a);
+    a.shift ? launch_dx_as<S, true, T>(a, g, stream) : launch_dx_as<S, false, T>(a, g, stream);
 }
 
 int input_gradient(DxArgs a, float* part, hipStream_t stream) {
@@ -383,26 +482,27 @@ int weight_gradient(DwArgs<T> a, float* part, hipStream_t stream) {
     return fqh::launched();
 }
 
-int products(const DxArgs& dx, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype, void* part,
+int products(const DxArgs& dx, const uint16_t* dy, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype, void* part,
              hipStream_t stream) {
     if (dx.dx) {
         const int st = input_gradient(dx, (float*)part, stream);
         if (st != FQ_OK || !dw) return st;
     }
     if (dw_dtype == FQ_F32)
-        return weight_gradient<float>({dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(float*)dw, (float*)dw2}, dx.m, dx.n, dx.k},
+        return weight_gradient<float>({dy, x, dx.ld, dx.cols, dx.run, ldx, {(float*)dw, (float*)dw2}, dx.m, dx.n, dx.k},
                                       (float*)part, stream);
     return weight_gradient<uint16_t>(
-        {dx.dy, x, dx.ld, dx.cols, dx.run, ldx, {(uint16_t*)dw, (uint16_t*)dw2}, dx.m, dx.n, dx.k}, (float*)part, stream);
+        {dy, x, dx.ld, dx.cols, dx.run, ldx, {(uint16_t*)dw, (uint16_t*)dw2}, dx.m, dx.n, dx.k}, (float*)part, stream);
 }
 
 }  // namespace
 
 size_t backward_workspace(int64_t m, int64_t n, int64_t k, bool gated) {
     const int64_t cols = gated ? 2 * padded(n, kDeep) : padded(n, 8);
-    const int64_t a = gated || n % 8 ? cols : 0, b = k % 8 ? padded(k, 8) : 0;
+    const int64_t a = gated ? 2 * cols : n % 8 ? cols : 0, b = k % 8 ? padded(k, 8) : 0;
+    const size_t powers = gated ? (size_t)(2 * cols * 4 + padded(m, 4) * 4) : 0;
     const size_t dx = cut_bytes(m, k, cols), dw = cut_bytes(cols, k, m);  // one after the other
-    return (size_t)(m * (a + b) * 2) + (dx > dw ? dx : dw);
+    return (size_t)(m * (a + b) * 2) + powers + (dx > dw ? dx : dw);
 }
 
 int matmul_backward(const void* dy, const void* x, int64_t m, int64_t n, int64_t k, int64_t group, const fql_w4* w,
@@ -412,22 +512,26 @@ int matmul_backward(const void* dy, const void* x, int64_t m, int64_t n, int64_t
     const uint16_t* xs = dw ? chunk_rows(x, m, k, at, stream) : nullptr;
     const W4Mat wm = dx ? w4_mat(*w, k, group) : W4Mat{};
     const int64_t ld = padded(n, 8);
-    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, dx, m, n, k}, xs, padded(k, 8), dw, nullptr, dw_dtype, at,
+    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, dx, m, n, k}, y, xs, padded(k, 8), dw, nullptr, dw_dtype, at,
                     stream);
 }
 
 int gated_backward(const void* dh, const void* x, const void* g, const void* u, int64_t m, int64_t n, int64_t k,
                    int64_t group, int act, const fql_w4* gate, const fql_w4* up, void* dx, void* dw_gate, void* dw_up,
                    int dw_dtype, void* workspace, hipStream_t stream) {
-    const int64_t run = padded(n, kDeep);
-    uint16_t* both = (uint16_t*)workspace;
-    char* at = (char*)(both + m * 2 * run);
-    k_gate_grad<<<fqh::grid_all(m * run / 8, 256), 256, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g,
-                                                                     (const uint16_t*)u, act, m, n, run, both);
+    const int64_t run = padded(n, kDeep), ng = (k + group - 1) / group;
+    uint16_t *half = (uint16_t*)workspace, *both = half + m * 2 * run;
+    float *up_by = (float*)(both + m * 2 * run), *down = up_by + 2 * run;
+    int32_t* shift = (int32_t*)(down + 2 * run);
+    char* at = (char*)(shift + padded(m, 4));
+    if (dx)
+        k_row_powers<<<(unsigned)((2 * run + 15) / 16), 256, 0, stream>>>(gate->scale, up->scale, n, run, ng, up_by, down);
+    k_gate_grad<<<(unsigned)m, 256, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, act, n, run,
+                                                 up_by, dx ? half : nullptr, shift, dw_gate ? both : nullptr);
     const uint16_t* xs = dw_gate ? chunk_rows(x, m, k, at, stream) : nullptr;
-    DxArgs a{both, 2 * run, 2 * run, run, {}, dx, m, n, k};
+    DxArgs a{half, 2 * run, 2 * run, run, {}, dx, m, n, k, 0, 0, 0, shift, down};
     if (dx) a.w[0] = w4_mat(*gate, k, group), a.w[1] = w4_mat(*up, k, group);
-    return products(a, xs, padded(k, 8), dw_gate, dw_up, dw_dtype, at, stream);
+    return products(a, both, xs, padded(k, 8), dw_gate, dw_up, dw_dtype, at, stream);
 }
 
 }  // namespace fqw

@@ -62,7 +62,18 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, float z16) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// The eight weights of a dword in bfloat16, rounded to nearest; s16 = 16 scale.
+// The eight weights of a dword in bfloat16 or half precision (whose bits are returned),
+// rounded to nearest; s16 = 16 scale.
+template <bool ZP>
+__device__ __forceinline__ bf16x8 weights_half(uint32_t w, float z16, float s16) {
+    const uint32_t hi = w >> 4;
+    float f[8] = {cvt_i4<0>(hi), cvt_i4<0>(w), cvt_i4<1>(hi), cvt_i4<1>(w),
+                  cvt_i4<2>(hi), cvt_i4<2>(w), cvt_i4<3>(hi), cvt_i4<3>(w)};
+    f16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)((ZP ? f[i] - z16 : f[i]) * s16);
+    return __builtin_bit_cast(bf16x8, r);
+}
 template <bool ZP>
 __device__ __forceinline__ bf16x8 weights_bf16(uint32_t w, float z16, float s16) {
     const uint32_t hi = w >> 4;
