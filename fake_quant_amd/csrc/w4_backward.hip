@@ -34,7 +34,7 @@ struct DwArgs {
     const uint16_t* x;   // [m] rows of k columns, ldx apart
     int64_t ld, cols, run, ldx;
     T* dw[2];
-    int64_t m, n, k;
+    int64_t m, n, k;  // k: columns of a row of dw (partial sums: padded to a multiple of 4)
     uint32_t ni, nj, steps;
 };
 
@@ -86,18 +86,21 @@ struct CodeSteps {
     // Codes 8 J .. of those to a tile.
     template <int J>
     __device__ __forceinline__ void store(uint16_t* tile, const CodeRegs& d) const {
-        const float z = ZP ? (float)(d.z & d.mask) * 0.0625f : 0.0f, s = d.none ? 0.0f : d.s * 16.0f;
+        const float s = d.none ? 0.0f : HALF ? d.s * d.down : d.s * 16.0f;
+        const float z = ZP ? (float)(d.z & d.mask) * (HALF ? 1.0f : 0.0625f) : 0.0f;
         *reinterpret_cast<bf16x8*>(tile + line * BN + by_steps(4 * part + J, line) * 8) =
-            HALF ? weights_half<ZP>(d.c[J], z, s * d.down) : weights_bf16<ZP>(d.c[J], z, s);
+            HALF ? weights_half(d.c[J], z, s) : weights_bf16<ZP>(d.c[J], z, s);
     }
 };
 
 // A wave's sums to its rows and columns of a tile in LDS: lanes hold one row each and
-// runs of four columns.  exponent(row) halves a row's sums that often.
-template <class S, class T, class Exponent>
+// runs of four columns.  HALF: the columns in the order of weights_half, and
+// exponent(row) halves a row's sums that often.
+template <class S, bool HALF, class T, class Exponent>
 __device__ __forceinline__ void put_sums(const f32x16 (&acc)[S::MS][S::NS], T* lds, int pitch, Exponent exponent) {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    T* at = lds + (wave / S::WN * (S::MS * 32) + lane % 32) * pitch + wave % S::WN * (S::NS * 32) + 4 * (lane / 32);
+    T* at = lds + (wave / S::WN * (S::MS * 32) + lane % 32) * pitch + wave % S::WN * (S::NS * 32) +
+            (HALF ? 2 : 4) * (lane / 32);
 #pragma unroll
     for (int i = 0; i < S::MS; ++i) {
         const int down = exponent(wave / S::WN * (S::MS * 32) + 32 * i + lane % 32);
@@ -105,7 +108,8 @@ __device__ __forceinline__ void put_sums(const f32x16 (&acc)[S::MS][S::NS], T* l
         for (int j = 0; j < S::NS; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                store_f(at + 32 * i * pitch + 32 * j + e / 4 * 8 + e % 4, __builtin_amdgcn_ldexpf(acc[i][j][e], -down));
+                store_f(at + 32 * i * pitch + 32 * j + e / 4 * 8 + (HALF ? half_column(e % 4) : e % 4),
+                        HALF ? __builtin_amdgcn_ldexpf(acc[i][j][e], -down) : acc[i][j][e]);
     }
 }
 struct NoExponent {
@@ -144,7 +148,8 @@ struct TileLds {
 
 // RAGGED: k is no multiple of 32, so that a thread's run of codes may end inside the
 // matrix (a branch that costs the others 30%: 177 against 135 us at 4096^3).
-// T: bfloat16 for dx itself; float for partial sums, one [m, k] matrix per blockIdx.y.
+// T: bfloat16 for dx itself; float for partial sums, one matrix of m rows of k, padded to
+// a multiple of 4, per blockIdx.y.
 template <class S, bool ZP, bool RAGGED, bool HALF, class T>
 __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     __shared__ TileLds<S, T> lds;
@@ -156,7 +161,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     DenseRows<S::BM, S::kThreads> ys(a.dy + l0, i0, a.m, a.ld, a.cols - l0, wave, lane);
     CodeSteps<S::BN, ZP, HALF> ws(a, j0, l0, t);
     const int wi = wave / S::WN * (S::MS * 32), wj = wave % S::WN * (S::NS * 32);
-    T* const dx = (T*)a.dx + blockIdx.y * a.m * a.k;
+    const int64_t pitch_out = sizeof(T) == 4 ? (a.k + 3) / 4 * 4 : a.k;
+    T* const dx = (T*)a.dx + blockIdx.y * a.m * pitch_out;
 
     f32x16 acc[S::MS][S::NS] = {};
     Frags<S> f[2];
@@ -207,11 +213,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     for (uint32_t st = 0; st < a.steps; ++st) stage(st & 1);  // past the end both operands are zeros
     wait_loads();
     OutTile<S, T, S::BN>::store(
-        lds.out, j0, a.k, [&](T* out, int pitch) {
-            if constexpr (HALF) put_sums<S>(acc, out, pitch, [&](int r) { return i0 + r < a.m ? a.shift[i0 + r] : 0; });
-            else put_sums<S>(acc, out, pitch, NoExponent{});
+        lds.out, j0, pitch_out, [&](T* out, int pitch) {
+            if constexpr (HALF) put_sums<S, true>(acc, out, pitch, [&](int r) { return i0 + r < a.m ? a.shift[i0 + r] : 0; });
+            else put_sums<S, false>(acc, out, pitch, NoExponent{});
         },
-        [&](int r) { return i0 + r < a.m ? dx + (i0 + r) * a.k : nullptr; });
+        [&](int r) { return i0 + r < a.m ? dx + (i0 + r) * pitch_out : nullptr; });
 }
 
 template <class S, class T>
@@ -263,7 +269,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
     }
     wait_loads();
     OutTile<S, T, S::BN>::store(
-        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S>(acc, out, pitch, NoExponent{}); },
+        lds.out, j0, a.k, [&](T* out, int pitch) { put_sums<S, false>(acc, out, pitch, NoExponent{}); },
         [&](int r) -> T* {
             const int64_t i = i0 + r, f = i < a.run ? i : i - a.run;
             return i < a.cols && f < a.n ? (i < a.run ? part : a.dw[1]) + f * a.k : nullptr;
@@ -292,39 +298,51 @@ __device__ __forceinline__ void gate_grad(const uint16_t* dh, const uint16_t* g,
 // For dw in bfloat16.  For dx in half precision, whose 11 bits (and the weights' there)
 // leave the sums as good as rounded once; bfloat16 on both sides would have added two
 // roundings of 2^-8 to that of dx.  Half precision spans little range, so each row of
-// a weight is divided by the power of two of its largest scale, dg and du are
-// multiplied by it, and each token is multiplied by 2^shift, which puts its largest
-// magnitude at 2^12 .. 2^13: what that loses lies 2^-37 under a token's largest value.
-// One workgroup per token forms the values twice, for the largest and to write them.
-__global__ __launch_bounds__(256) void k_gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
+// a weight is divided by the power of two that puts its largest scale at 2^10 .. 2^11
+// (its weights under 2^15), dg and du are multiplied by it, and each token is multiplied
+// by 2^shift, which puts its largest magnitude at 2^12 .. 2^13.  Scales keep all bits down to
+// 2^-24 of their row's largest, and what a token loses lies 2^-37 under its largest value.
+// One workgroup per token holds what its threads formed while the largest is found (a
+// row of up to 16384), or forms it again.
+__global__ __launch_bounds__(512) void k_gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
                                                    int64_t n, int64_t run, const float* up, uint16_t* half,
                                                    int32_t* shift, uint16_t* out) {
-    __shared__ float wave_max[4];
+    constexpr int kHeld = 4, kStride = 512 * 8;
+    __shared__ float wave_max[8];
     const int64_t r = blockIdx.x, at = r * n;
+    const bool held = run <= kHeld * kStride;
+    float dg[kHeld][8], du[kHeld][8];
+    float top = 0.0f;
+    const auto form = [&](int64_t c, float(&a)[8], float(&b)[8]) {
+        gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, a, b);
+        if (!half) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = fabsf(a[i] * up[c + i]), q = fabsf(b[i] * up[run + c + i]);
+            if (p < INFINITY) top = fmaxf(top, p);
+            if (q < INFINITY) top = fmaxf(top, q);
+        }
+    };
+    if (held) {
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int64_t c = threadIdx.x * 8 + h * kStride;
+            if (c < run) form(c, dg[h], du[h]);
+        }
+    } else if (half) {
+        for (int64_t c = threadIdx.x * 8; c < run; c += kStride) form(c, dg[0], du[0]);
+    }
     int sh = 0;
     if (half) {
-        float top = 0.0f;
-        for (int64_t c = threadIdx.x * 8; c < n; c += 2048) {
-            float dg[8], du[8];
-            gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, dg, du);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = fabsf(dg[i] * up[c + i]), b = fabsf(du[i] * up[run + c + i]);
-                if (a < INFINITY) top = fmaxf(top, a);
-                if (b < INFINITY) top = fmaxf(top, b);
-            }
-        }
 #pragma unroll
         for (int o = 32; o; o /= 2) top = fmaxf(top, __shfl_xor(top, o));
         if (threadIdx.x % 64 == 0) wave_max[threadIdx.x / 64] = top;
         __syncthreads();
-        top = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, wave_max[w]);
         if (top > 0.0f) sh = 13 - __builtin_amdgcn_frexp_expf(top);
         if (threadIdx.x == 0) shift[r] = sh;
     }
-    for (int64_t c = threadIdx.x * 8; c < run; c += 2048) {
-        float dg[8], du[8];
-        gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, dg, du);
+    const auto write = [&](int64_t c, const float(&dg)[8], const float(&du)[8]) {
         if (out) {
             bf16x8 a, b;
 #pragma unroll
@@ -342,12 +360,24 @@ __global__ __launch_bounds__(256) void k_gate_grad(const uint16_t* dh, const uin
             *reinterpret_cast<f16x8*>(half + r * 2 * run + c) = a;
             *reinterpret_cast<f16x8*>(half + r * 2 * run + run + c) = b;
         }
+    };
+    if (held) {
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int64_t c = threadIdx.x * 8 + h * kStride;
+            if (c < run) write(c, dg[h], du[h]);
+        }
+    } else {
+        for (int64_t c = threadIdx.x * 8; c < run; c += kStride) {
+            gate_grad(dh + at + c, g + at + c, u + at + c, act, n - c, dg[0], du[0]);
+            write(c, dg[0], du[0]);
+        }
     }
 }
 
-// up[i]: the power of two of the largest finite scale of row i of two weights, one
-// below the other in `run` rows each (1 where there is none); down[i] = 1 / up[i].
-// 16 lanes a row.
+// up[i]: the power of two by which the largest finite scale of row i of two weights, one
+// below the other in `run` rows each, is 2^10 .. 2^11 (1 where there is none); down[i] =
+// 1 / up[i].  16 lanes a row.
 __global__ __launch_bounds__(256) void k_row_powers(const float* gate, const float* below, int64_t n, int64_t run,
                                                     int64_t ng, float* up, float* down) {
     const int64_t i = blockIdx.x * 16ll + threadIdx.x / 16, r = i < run ? i : i - run;
@@ -359,7 +389,7 @@ __global__ __launch_bounds__(256) void k_row_powers(const float* gate, const flo
     }
 #pragma unroll
     for (int o = 8; o; o /= 2) top = fmaxf(top, __shfl_xor(top, o, 16));
-    int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
+    int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 11 : 0;
     e = e < -120 ? -120 : e > 120 ? 120 : e;
     if (threadIdx.x % 16 == 0) {
         up[i] = __builtin_amdgcn_ldexpf(1.0f, e);
@@ -391,17 +421,23 @@ const uint16_t* chunk_rows(const void* p, int64_t rows, int64_t cols, char*& at,
     return out;
 }
 
-// The sum of `splits` matrices of `rows` rows of k, rows run .. of it in out2.
+// The sum of `splits` matrices of `rows` rows, kp = k padded to a multiple of 4 apart; rows run .. in out2.
 template <class T>
 __global__ __launch_bounds__(256) void k_join(const float* part, int splits, int64_t rows, int64_t n, int64_t run,
-                                              int64_t k, T* out, T* out2) {
-    const int64_t all = rows * k;
-    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < all; v += gridDim.x * 256ll) {
-        const int64_t i = v / k, f = i < run ? i : i - run;
+                                              uint32_t k, uint32_t kp, T* out, T* out2) {
+    const int64_t all = rows * kp;
+    const uint32_t wide = kp / 4;
+    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < rows * wide; v += gridDim.x * 256ll) {
+        const int64_t i = v < (int64_t)1 << 32 ? (uint32_t)v / wide : v / wide, f = i < run ? i : i - run;
         if (f >= n) continue;
-        float sum = part[v];
-        for (int p = 1; p < splits; ++p) sum += part[p * all + v];
-        store_f((i < run ? out : out2) + f * k + v % k, sum);
+        const uint32_t c = (uint32_t)(v - i * wide) * 4;
+        f32x4 sum = *reinterpret_cast<const f32x4*>(part + i * kp + c);
+#pragma unroll 8
+        for (int p = 1; p < splits; ++p) sum += *reinterpret_cast<const f32x4*>(part + p * all + i * kp + c);
+        T* to = (i < run ? out : out2) + f * k + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < k) store_f(to + e, sum[e]);
     }
 }
 
@@ -417,15 +453,15 @@ Cut cut(int64_t rows, int64_t cols, int64_t deep) {
     const bool big = big_tiles(rows, cols);
     const int64_t all = (deep + kDeep - 1) / kDeep, mid = ((rows + 127) / 128) * ((cols + 255) / 256);
     // A few tiles leave most compute units idle: their sums are split into pieces of
-    // four steps or more until the units are busy, and joined by a second kernel.
-    int64_t splits = big || mid > kUnits / 2 ? 1 : kUnits / mid < all / 4 ? kUnits / mid : all / 4;
+    // two steps or more until the units are busy, and joined by a second kernel.
+    int64_t splits = big || mid > kUnits / 2 || all < 4 ? 1 : kUnits / mid < all / 2 ? kUnits / mid : all / 2;
     if (splits < 2) return {big, (uint32_t)all, 1};
     const int64_t steps = ((all + splits - 1) / splits + 1) / 2 * 2;
     return {false, (uint32_t)steps, (uint32_t)((all + steps - 1) / steps)};
 }
 size_t cut_bytes(int64_t rows, int64_t cols, int64_t deep) {
     const Cut c = cut(rows, cols, deep);
-    return c.splits > 1 ? (size_t)(c.splits * rows * cols * 4 + 15) / 16 * 16 : 0;
+    return c.splits > 1 ? (size_t)(c.splits * rows * padded(cols, 4) * 4) : 0;
 }
 
 template <class S, bool HALF, class T>
@@ -458,7 +494,9 @@ int input_gradient(DxArgs a, float* part, hipStream_t stream) {
         uint16_t* dx = (uint16_t*)a.dx;
         a.dx = part;
         launch_dx<Mid, float>(a, g, stream);
-        k_join<<<fqh::grid_all(a.m * a.k, 256), 256, 0, stream>>>(part, (int)c.splits, a.m, a.m, a.m, a.k, dx, dx);
+        const int64_t kp = padded(a.k, 4);
+        k_join<<<fqh::grid_all(a.m * kp / 4, 256), 256, 0, stream>>>(part, (int)c.splits, a.m, a.m, a.m, (uint32_t)a.k,
+                                                                     (uint32_t)kp, dx, dx);
     }
     return fqh::launched();
 }
@@ -475,9 +513,11 @@ int weight_gradient(DwArgs<T> a, float* part, hipStream_t stream) {
     } else if (c.splits == 1) {
         k_dw<Mid, T><<<g, Mid::kThreads, 0, stream>>>(a);
     } else {
-        const DwArgs<float> p{a.dy, a.x, a.ld, a.cols, a.cols, a.ldx, {part, part}, a.m, a.cols, a.k, a.ni, a.nj, a.steps};
+        const int64_t kp = padded(a.k, 4);
+        const DwArgs<float> p{a.dy, a.x, a.ld, a.cols, a.cols, a.ldx, {part, part}, a.m, a.cols, kp, a.ni, a.nj, a.steps};
         k_dw<Mid, float><<<g, Mid::kThreads, 0, stream>>>(p);
-        k_join<<<fqh::grid_all(a.cols * a.k, 256), 256, 0, stream>>>(part, (int)c.splits, a.cols, a.n, a.run, a.k, a.dw[0], a.dw[1]);
+        k_join<<<fqh::grid_all(a.cols * kp / 4, 256), 256, 0, stream>>>(part, (int)c.splits, a.cols, a.n, a.run, (uint32_t)a.k,
+                                                                        (uint32_t)kp, a.dw[0], a.dw[1]);
     }
     return fqh::launched();
 }
@@ -526,7 +566,7 @@ int gated_backward(const void* dh, const void* x, const void* g, const void* u, 
     char* at = (char*)(shift + padded(m, 4));
     if (dx)
         k_row_powers<<<(unsigned)((2 * run + 15) / 16), 256, 0, stream>>>(gate->scale, up->scale, n, run, ng, up_by, down);
-    k_gate_grad<<<(unsigned)m, 256, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, act, n, run,
+    k_gate_grad<<<(unsigned)m, 512, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, act, n, run,
                                                  up_by, dx ? half : nullptr, shift, dw_gate ? both : nullptr);
     const uint16_t* xs = dw_gate ? chunk_rows(x, m, k, at, stream) : nullptr;
     DxArgs a{half, 2 * run, 2 * run, run, {}, dx, m, n, k, 0, 0, 0, shift, down};

@@ -153,3 +153,37 @@ def test_nonfinite_tokens_of_tiles(lin):
         log(f"nonfinite tile {dtype}")
         y = lin.w4_matmul(x.cuda(), w, group)
         ref.assert_within(y, *ref.matmul(x, wd), "y")
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 2.0 ** -20, 2.0 ** 12])
+def test_uneven_scales(lin, ratio):
+    """Groups and rows of a weight far from the others', and tokens far from each other."""
+    m, n, k, group = 70, 300, 256, 64
+    ws = []
+    for seed in (1, 2):
+        w = ref.weight(n, k, group, "affine", seed)
+        w["scale"][:, 1] *= ratio
+        w["scale"][::3] *= ratio
+        ws.append((ref.to(w, "cuda"), ref.dense(w, k, group)))
+    (wg, gd), (wu, ud) = ws
+    x, dh = ref.tokens(m, k, BF, 3), ref.tokens(m, n, BF, 4, 1e-3)
+    dh[::2] *= ratio
+    g, u = ref.tokens(m, n, BF, 5, 2.0), ref.tokens(m, n, BF, 6)
+    log(f"uneven scales {ratio}")
+    got = lin.w4_gated_backward(dh.cuda(), x.cuda(), g.cuda(), u.cuda(), wg, wu, group)
+    want, bound = ref.gated_backward(dh, x, g, u, gd, ud, "silu", BF)
+    for name, o, w_, b in zip(("dx", "dwg", "dwu"), got, want, bound):
+        ref.assert_within(o, w_, b, name)
+
+
+def test_long_rows(lin):
+    """Tokens of more than 16384 values of g and u."""
+    m, n, k, group = 5, 17000, 64, 32
+    (wg, gd), (wu, ud) = sides(n, k, group, "sym", 1), sides(n, k, group, "affine", 2)
+    x, dh = ref.tokens(m, k, BF, 3), ref.tokens(m, n, BF, 4, 1e-3)
+    g, u = ref.tokens(m, n, BF, 5, 2.0), ref.tokens(m, n, BF, 6)
+    log("long rows")
+    got = lin.w4_gated_backward(dh.cuda(), x.cuda(), g.cuda(), u.cuda(), wg, wu, group)
+    want, bound = ref.gated_backward(dh, x, g, u, gd, ud, "silu", BF)
+    for name, o, w_, b in zip(("dx", "dwg", "dwu"), got, want, bound):
+        ref.assert_within(o, w_, b, name)
