@@ -176,10 +176,10 @@ __device__ __forceinline__ bf16x8 frag_steps(uint16_t* tile, int row, int s, int
 }
 
 // A tile of BM x COLS outputs on its way through LDS, so that memory sees whole rows.
-template <class S, class T, int COLS>
+template <class S, class T, int COLS, int PAD = 16 / sizeof(T)>
 struct OutTile {
     // one pass where the tile fits beside 160 KiB, or a pass for the waves of each tile row
-    static constexpr int kPitch = COLS + 16 / sizeof(T);
+    static constexpr int kPitch = COLS + PAD;
     static constexpr int kPasses = S::BM * kPitch * sizeof(T) > 150000 ? S::WM : 1;
     static constexpr int kRows = S::BM / kPasses, kSize = kRows * kPitch;
     // put(tile, pitch): a wave's outputs; row(r): where row r of the tile goes, or null.
