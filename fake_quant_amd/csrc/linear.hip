@@ -1,8 +1,9 @@
 // linear.hip -- C entry points of the products with 4-bit group-quantized
 // weights (fq_linear.h): argument checks and the choice of a kernel, and the
-// kernel that serves every shape.
+// kernel that serves every shape: groups that are no multiple of 32 columns, bases off
+// 16-byte borders, weights of a few bytes, widths of 2^20 and more.
 //
-// The kernel: C[i, j] = sum_l A(i, l) B(j, l) in binary32 on a 64 x 64 tile of
+// That kernel: C[i, j] = sum_l A(i, l) B(j, l) in binary32 on a 64 x 64 tile of
 // LDS, 16 sums per thread.  A and B are any functions of two indices (a dense
 // matrix, its transpose, a stored 4-bit matrix, a gradient formed from dh, g, u).
 #include "fq_host.h"

@@ -1,11 +1,18 @@
-// w4_few.hip -- products of few token rows (up to 64) with 4-bit group-quantized
-// weights: y = x W^T and the gated block, for single-token serving and small batches.
+// w4_few.hip -- products of few token rows with 4-bit group-quantized weights: y = x W^T
+// and the gated block, for single-token serving and small batches.
 //
-// What bounds it: the codes, k / 2 bytes per row of W, read once; at 64 tokens
-// still only 256 products per byte.  A workgroup owns 16 NT rows of W (of both
-// weights for the gated block) and its waves deal the row's 128-column steps
-// among them, so a 4096 x 4096 weight spreads over all 256 compute units with
-// every load in flight at once; the waves' partial sums meet in LDS in wave order.
+// What bounds it: one token, the codes, k / 2 bytes per row of W, read once, and their
+// decoding; more tokens, how often x is read (every 16 NT rows of W) and the decoding.
+// A workgroup owns 16 NT rows of W (of both weights for the gated block) and its eight
+// waves take runs of the rows' 128-column steps, so a 4096 x 4096 weight spreads over
+// all 256 compute units; the waves' sums meet in LDS in wave order.
+//
+// Measured (kernel time, inputs in the last-level cache): 1 token 4096 x 4096, groups of
+// 128: 4.7 us (an empty launch takes about 2); 1 token 4096 x 12288 affine, groups of 64:
+// 10.5 us, 3.0 TB/s; 1 token of a gated block 12288 x 4096: 13.5 .. 15.5 us, 3.7 TB/s; 48
+// tokens 8192 x 4096 affine: 13.4 us.  Before the loads were dealt four lanes a row (see
+// FewWave): 5.6, 20.2, 20.4 and 33.5 us.  Starting the workgroups at different columns, to
+// spread memory channels, changed nothing.
 #include "fq_host.h"
 #include "w4_mfma.h"
 #include "w4_linear.h"
@@ -293,6 +300,10 @@ int launch(const FewArgs<T>& a, int64_t group, hipStream_t stream) {
 
 template <class T, int W>
 int few(const FewArgs<T>& a, int64_t group, hipStream_t stream) {
+    // More tokens a workgroup read W less often, more rows of W read x less often; fewer
+    // rows keep more compute units busy.  Rows of 48 tokens, 8192 x 4096: 16 x 4 tokens by
+    // 32 rows 13.3 us, by 16 18.9, by 64 20.0; 64 float32 tokens, 4096 x 4096: 8 x 4 tokens by
+    // 32 rows 19.4 us, by 16 30.7; 24 tokens there: 8 x 4 tokens 8.4 us, 16 x 4 11.4.
     if (a.m <= 4) return launch<T, 1, 1, W, 4>(a, group, stream);
     if constexpr (sizeof(T) == 4) return a.m <= 16 ? launch<T, 4, 1, W, 1>(a, group, stream) : launch<T, 8, 2 / W, W, 1>(a, group, stream);
     if (a.m <= 16) return launch<T, 4, 1, W, 2>(a, group, stream);

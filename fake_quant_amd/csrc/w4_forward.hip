@@ -1,10 +1,18 @@
 // w4_forward.hip -- products of many token rows with 4-bit group-quantized
 // weights: y = x W^T and the gated block, for prompts and training steps.
 //
-// What bounds it: the matrix instructions, 2 m n k operations.  Codes become exact
-// bfloat16 integers on their way into LDS, once per tile; each span's sum (64
-// columns, or 32 where groups are that fine) is multiplied by its scale as it
-// joins the tile's sum, so no weight is rounded.
+// What bounds it: the matrix instructions, 2 m n k operations, and beside them the
+// vector unit.  Codes become exact bfloat16 integers on their way into LDS, once per
+// tile; each span's sum (64 columns, or 32 where groups are that fine) is multiplied by
+// its scale as it joins the tile's sum, so no weight is rounded.  The order of a step is
+// what makes it fast: products that need nothing but LDS first, the next step's loads
+// behind them, decoding of the next step's codes between the products, no result of a
+// load touched before the step's end.
+//
+// Measured at 4096^3 (kernel time): groups of 128 or 64, symmetric 138 us, 1.0 PFLOP/s
+// (decoding before the products 158 us); affine 160 (200); groups of 32 affine 192 (222).  The
+// matrix units are busy half of the time at 2.0 GHz.  Gated block, 4096 tokens, 12288 x 4096:
+// 840 us, 0.98 PFLOP/s.  float32 x (three products for one): 420 us.
 #include "fq_host.h"
 #include "w4_linear.h"
 #include "w4_tile.h"

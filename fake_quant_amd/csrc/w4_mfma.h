@@ -1,20 +1,23 @@
 // w4_mfma.h -- how the matrix-instruction kernels read stored 4-bit weights and
 // token rows.
 //
-// One step of a kernel is 128 columns of W for 16 of its rows: lane l of a wave
-// holds 16 bytes (32 codes) of row l % 16, columns 32 (l / 16) .. + 31 of the step.
-// v_mfma_f32_16x16x32_bf16 takes 8 consecutive summation indices per lane, so a
-// lane's four dwords feed four instructions, and any assignment of the step's
-// columns to (instruction, lane) works as long as the token side follows it:
+// Codes become bfloat16 through v_cvt_off_f32_i4, which gives code / 16 exactly; the
+// difference code - zero_point is an integer of at most 15 in magnitude, exact in
+// bfloat16.  Products with a bfloat16 x are exact in binary32, and the group's scale
+// (times 16) multiplies the group's sum: nothing is rounded but the sums.  Eight codes
+// take 13 instructions, 21 with a zero-point, of 4 cycles a wave (2 for the float
+// differences).
+//
+// The few-token kernel takes 128 columns of W for 16 of its rows a step: lane l of a
+// wave holds 16 bytes (32 codes) of row l % 16, columns 32 (l / 16) .. + 31.
+// v_mfma_f32_16x16x32_bf16 takes 8 consecutive summation indices per lane, so a lane's
+// four dwords feed four instructions, and any assignment of the step's columns to
+// (instruction, lane) works as long as the token side follows it:
 //   Span 128: dword j of lane quarter q is columns 32 q + 8 j .. + 7;
 //   Span 64 / 32: the dwords are transposed between the lane quarters first (two
 //   permlane32 and two permlane16 swaps), so instruction j covers the 32
 //   consecutive columns 32 j .. + 31 and a group sum can end after one (32) or two
 //   (64) instructions.
-// Codes become bfloat16 through v_cvt_off_f32_i4, which gives code / 16 exactly;
-// the difference code - zero_point is an integer of at most 15 in magnitude, exact
-// in bfloat16.  Products with a bfloat16 x are exact in binary32, and the group's
-// scale (times 16) multiplies the group's sum: nothing is rounded but the sums.
 #pragma once
 
 #include "w4_device.h"
@@ -130,7 +133,6 @@ template <>
 struct Tokens<uint16_t> {
     static constexpr int kParts = 1;
     u32x4 v;
-    __device__ __forceinline__ void load(const uint16_t* s) { v = load16(s); }
     __device__ __forceinline__ void load_part(const uint16_t* s, int64_t n) {
         v = load16_part(reinterpret_cast<const uint8_t*>(s), 2 * n);
     }

@@ -19,15 +19,17 @@
  * with m rows and zeros to the gradients of the weights.
  *
  * Alignment: x, y, h, g, u, dy, dh, dx to their element size, scale and
- * zero_point to 4 bytes, codes to any; the workspace to 16 bytes.
+ * zero_point to 4 bytes, codes to any; the workspace to 16 bytes.  Groups of a multiple of
+ * 32 columns (or of whole rows) and 16-byte aligned matrices take the matrix
+ * instructions; anything else takes a kernel about twenty times slower at large sizes.
  *
  * Numbers: sums are held in binary32 and every output is rounded once to its
  * type, ties to even.  Products of x with the integers code - zero_point are exact
  * (a float32 x is split into three bfloat16 parts that sum to it), the scale
- * multiplies each group's sum.  Inf and NaN in x, dy, dh, g or u give the Inf and
- * NaN that the formulas give in the outputs whose sums hold them.  A backward pass
- * rounds its factors; each entry point says how.  Two calls on the same arguments
- * give the same bits.
+ * multiplies each group's sum, for any number of tokens.  Inf and NaN in x, dy, dh, g
+ * or u give the Inf and NaN that the formulas give in the outputs whose sums hold
+ * them.  A backward pass rounds its factors; each entry point says how.  Two calls on
+ * the same arguments give the same bits.
  */
 #ifndef FQ_LINEAR_H
 #define FQ_LINEAR_H
@@ -73,7 +75,7 @@ int fql_w4_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int6
 /* Gradients of y = x W^T: dx = dy W (bfloat16 [m, k]) and dw = dy^T x ([n, k] of
  * type dw_dtype, FQ_F32 or FQ_BF16), the latter the straight-through gradient of
  * the weights that were quantized (min / max calibration leaves none outside its
- * window).  dy [m, n] and x [m, k] bfloat16 (dtype other than FQ_BF16:
+ * window).  dx's sums hold W rounded to bfloat16; dw's products are exact.  dy [m, n] and x [m, k] bfloat16 (dtype other than FQ_BF16:
  * FQ_E_UNSUPPORTED).  dx or dw may be NULL, not both; x may be NULL without dw, w
  * without dx. */
 int fql_w4_matmul_backward(const void* dy, const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group,
@@ -84,7 +86,9 @@ int fql_w4_matmul_backward(const void* dy, const void* x, int dtype, int64_t m, 
  * that it wrote:
  *   dg = dh u act'(g), du = dh act(g);  dx = dg Wg + du Wu (bfloat16 [m, k]),
  *   dw_gate = dg^T x, dw_up = du^T x ([n, k] of type dw_dtype).
- * Inputs bfloat16 (dtype as above).  dx, or the two dw together, may be NULL. */
+ * Inputs bfloat16 (dtype as above).  dx, or the two dw together, may be NULL.  dx's sums
+ * hold dg, du and W rounded to half precision (of 11 bits, under a power of two per token and
+ * per row of W); those of the weights hold dg and du rounded to bfloat16. */
 int fql_w4_gated_backward(const void* dh, const void* x, const void* g, const void* u, int dtype, int64_t m, int64_t n,
                           int64_t k, int64_t group, int act, const fql_w4* gate, const fql_w4* up, void* dx,
                           void* dw_gate, void* dw_up, int dw_dtype, void* workspace, size_t workspace_bytes,

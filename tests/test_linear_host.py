@@ -155,3 +155,25 @@ def test_helper_refusals(lin):
     refused(lin.E_UNSUPPORTED, lin.w4_matmul_backward, torch.zeros(4, 8), x, w, 32, dw_dtype=torch.float16)
     d = torch.zeros(4, 8)
     refused(lin.E_DIM, lin.w4_gated_backward, d, x, d, torch.zeros(3, 8), w, w, 32)
+
+
+def test_workspace_refusals_of_tiles(lin):
+    """Sizes whose kernels need a workspace, beyond test_workspace_refusals."""
+    w, _ = weights(lin)
+    m, n, k, g = 2100, 2000, 72, 32
+    calls = [
+        (lin.fql_w4_matmul_workspace_bytes(0, m, n, k, g),
+         lambda ws, b: lin._lib.fql_w4_matmul(P, 0, m, n, k, g, w, P, ws, b, None)),
+        (lin.fql_w4_matmul_workspace_bytes(1, m, n, 77, g),
+         lambda ws, b: lin._lib.fql_w4_matmul(P, 1, m, n, 77, g, w, P, ws, b, None)),
+        (lin.fql_w4_gated_workspace_bytes(0, m, n, k, g),
+         lambda ws, b: lin._lib.fql_w4_gated(P, 0, m, n, k, g, 0, w, w, P, None, None, ws, b, None)),
+        (lin.fql_w4_matmul_backward_workspace_bytes(m, 77, k, g),
+         lambda ws, b: lin._lib.fql_w4_matmul_backward(P, P, 1, m, 77, k, g, w, P, P, 0, ws, b, None)),
+        (lin.fql_w4_gated_backward_workspace_bytes(m, n, k, g),
+         lambda ws, b: lin._lib.fql_w4_gated_backward(P, P, P, P, 1, m, n, k, g, 0, w, w, P, P, P, 1, ws, b, None)),
+    ]
+    for need, call in calls:
+        assert need > 0 and need % 16 == 0
+        for ws, b in ((None, need), (P, need - 1), (P + 8, need)):
+            assert call(ws, b) == lin.E_INVALID
