@@ -102,7 +102,7 @@ struct FewWave {
             for (int t = 0; t < kTiles; ++t) {
                 const int64_t at = wrow(t, lane / 4) * a.w[0].ng + g;
                 d.s[t][i] = a.w[t / NT].scale[at];
-                if constexpr (ZP) d.z[t][i] = a.zp[t / NT][at] & a.mask[t / NT];
+                if constexpr (ZP) d.z[t][i] = a.zp[t / NT][at];
             }
         }
     }
@@ -118,7 +118,7 @@ struct FewWave {
             for (int i = 0; i < kStats; ++i) {
                 const int at = lane / 4 * kPitch + 4 * i + lane % 4;
                 lds.s[t][at] = d.s[t][i] * 16.0f;
-                if constexpr (ZP) lds.z[t][at] = (float)d.z[t][i] * 0.0625f;
+                if constexpr (ZP) lds.z[t][at] = (float)(d.z[t][i] & a.mask[t / NT]) * 0.0625f;
             }
         turn();
     }
