@@ -54,41 +54,50 @@ struct CodeRegs {
 };
 template <int BN, bool ZP, bool HALF>
 struct CodeSteps {
-    static constexpr int kParts = BN / 32, kLoads = ZP ? 3 : 2;
+    static constexpr int kParts = BN / 32;
     const DxArgs& a;
-    int64_t byte, gi, l0;
+    int64_t l0;
+    uint32_t codes, scales;  // offsets of the thread's row and columns from a step's first row
     int line, part;
     __device__ __forceinline__ CodeSteps(const DxArgs& a_, int64_t col0, int64_t l0_, int t)
         : a(a_), l0(l0_), line(t / kParts), part(t % kParts) {
         const int64_t col = col0 + 32 * part;
-        byte = col / 2;
-        gi = (col < a.k ? col : a.k - 1) / a.w[0].group;
+        codes = (uint32_t)(line * a.w[0].row_bytes + col / 2);
+        scales = (uint32_t)(line * a.w[0].ng + (col < a.k ? col : a.k - 1) / a.w[0].group);
     }
-    // The thread's row at step l0, and the bytes of the matrix from its codes there on.
-    __device__ __forceinline__ int64_t row_at(int64_t step, int64_t& left) const {
-        const int64_t r = step - (step >= a.run ? a.run : 0) + line, at = r < a.n ? r : a.n - 1;
-        left = (a.n - at) * a.w[0].row_bytes - byte;
-        return r;
+    // The matrix of step l0, its first row there (the last one, past the matrix), and the
+    // bytes of the matrix from there on, as far as a step may reach.
+    __device__ __forceinline__ int64_t rows_at(int64_t step, int& which, uint32_t& bytes) const {
+        which = step >= a.run;  // a step lies in one of the matrices
+        const int64_t r = step - (which ? a.run : 0), first = r < a.n ? r : a.n - 1;
+        const int64_t left = (a.n - first) * a.w[0].row_bytes;
+        bytes = left < (1 << 30) ? (uint32_t)left : 1u << 30;
+        return first;
     }
     // The codes of the present step; then the next one is present.  Nothing here reads
     // what was loaded: that would wait for it.
     __device__ __forceinline__ void load(CodeRegs& d) {
-        const int which = l0 >= a.run;  // a step lies in one of the matrices
-        int64_t left;
-        const int64_t r = row_at(l0, left), at = r < a.n ? r : a.n - 1;
+        int which;
+        uint32_t bytes;
+        const int64_t first = rows_at(l0, which, bytes);
         // past the matrix a thread reads its last 16 bytes, which whole() puts in place
-        d.c = load16(a.w[which].codes + at * a.w[0].row_bytes + (left < 16 ? byte + left - 16 : byte));
-        d.s = a.w[which].scale[at * a.w[0].ng + gi];
-        if constexpr (HALF) d.down = a.down[(which ? a.run : 0) + at];
-        if constexpr (ZP) d.z = a.zp[which][at * a.w[0].ng + gi], d.mask = a.mask[which];
-        d.none = r >= a.n || l0 >= a.cols;
+        const uint32_t at = codes + 16 < bytes ? codes + 16 : bytes;
+        d.c = load16(a.w[which].codes + first * a.w[0].row_bytes - 16 + at);
+        const int64_t rows = a.n - first;
+        const uint32_t last = (uint32_t)((rows < kDeep ? rows : kDeep) * a.w[0].ng - 1), i = scales < last ? scales : last;
+        d.s = a.w[which].scale[first * a.w[0].ng + i];
+        if constexpr (ZP) d.z = a.zp[which][first * a.w[0].ng + i], d.mask = a.mask[which];
+        if constexpr (HALF) d.down = a.down[(which ? a.run : 0) + first + (line < rows ? line : 0)];
+        d.none = l0 - (which ? a.run : 0) + line >= a.n || l0 >= a.cols;
         l0 += kDeep;
     }
     // Puts in place what the last load() read.
     __device__ __forceinline__ void whole(CodeRegs& d) const {
-        int64_t left;
-        row_at(l0 - kDeep, left);
-        if (left < 16) d.c = drop_bytes(d.c, left <= 0 ? 16 : 16 - (int)left);
+        int which;
+        uint32_t bytes;
+        rows_at(l0 - kDeep, which, bytes);
+        const int past = (int)(codes + 16) - (int)bytes;
+        if (past > 0) d.c = drop_bytes(d.c, past < 16 ? past : 16);
     }
     // Codes 8 J .. of those to a tile.
     template <int J>
@@ -137,8 +146,8 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MS][S::NS], const Frag
 #pragma unroll
             for (int j = 0; j < S::NS; ++j)
                 if constexpr (HALF)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, f.b[j][h]),
-                                                                       __builtin_bit_cast(f16x8, f.a[i][h]), acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(f16x8, f.b[j][h]), __builtin_bit_cast(f16x8, f.a[i][h]), acc[i][j], 0, 0, 0);
                 else
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j][h], f.a[i][h], acc[i][j], 0, 0, 0);
 }
@@ -179,7 +188,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < S::NS; ++j) d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
+            for (int j = 0; j < S::NS; ++j)
+                d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
 #pragma unroll
             for (int i = 0; i < S::MS; ++i) d.a[i][h] = frag_rows(lds.a[stage], wi + 32 * i, 2 * half + h, lane);
         }
@@ -221,8 +231,10 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dx(DxArgs a) {
     wait_loads();
     OutTile<S, T, S::BN>::store(
         lds.out, j0, pitch_out, [&](T* out, int pitch) {
-            if constexpr (HALF) put_sums<S, true>(acc, out, pitch, [&](int r) { return i0 + r < a.m ? a.shift[i0 + r] : 0; });
-            else put_sums<S, false>(acc, out, pitch, NoExponent{});
+            if constexpr (HALF)
+                put_sums<S, true>(acc, out, pitch, [&](int r) { return i0 + r < a.m ? a.shift[i0 + r] : 0; });
+            else
+                put_sums<S, false>(acc, out, pitch, NoExponent{});
         },
         [&](int r) { return i0 + r < a.m ? dx + (i0 + r) * pitch_out : nullptr; });
 }
@@ -246,9 +258,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < S::NS; ++j) d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
+            for (int j = 0; j < S::NS; ++j)
+                d.b[j][h] = frag_steps<S::BN>(lds.b[stage], wj + 32 * j, 2 * half + h, lane);
 #pragma unroll
-            for (int i = 0; i < S::MS; ++i) d.a[i][h] = frag_steps<S::BM>(lds.a[stage], wi + 32 * i, 2 * half + h, lane);
+            for (int i = 0; i < S::MS; ++i)
+                d.a[i][h] = frag_steps<S::BM>(lds.a[stage], wi + 32 * i, 2 * half + h, lane);
         }
     };
     const uint32_t at[2] = {lds_address(lds.a[0]), lds_address(lds.a[1])};
@@ -284,8 +298,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_dw(DwArgs<T> a) {
 }
 
 // dg and du of eight columns from c on, zeros past the row's end.
-__device__ __forceinline__ void gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act, int64_t left,
-                                          float (&dg)[8], float (&du)[8]) {
+__device__ __forceinline__ void gate_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
+                                          int64_t left, float (&dg)[8], float (&du)[8]) {
     Tokens<uint16_t> td, tg, tu;
     td.load_part(dh, left), tg.load_part(g, left), tu.load_part(u, left);
     bf16x8 d[1], gg[1], uu[1];
@@ -475,8 +489,12 @@ template <class S, bool HALF, class T>
 void launch_dx_as(const DxArgs& a, dim3 g, hipStream_t stream) {
     const bool zp = a.w[0].zp || a.w[1].zp;
     const dim3 b(S::kThreads);
-    if (a.k % 32) zp ? k_dx<S, true, true, HALF, T><<<g, b, 0, stream>>>(a) : k_dx<S, false, true, HALF, T><<<g, b, 0, stream>>>(a);
-    else zp ? k_dx<S, true, false, HALF, T><<<g, b, 0, stream>>>(a) : k_dx<S, false, false, HALF, T><<<g, b, 0, stream>>>(a);
+    if (a.k % 32)
+        zp ? k_dx<S, true, true, HALF, T><<<g, b, 0, stream>>>(a)
+           : k_dx<S, false, true, HALF, T><<<g, b, 0, stream>>>(a);
+    else
+        zp ? k_dx<S, true, false, HALF, T><<<g, b, 0, stream>>>(a)
+           : k_dx<S, false, false, HALF, T><<<g, b, 0, stream>>>(a);
 }
 template <class S, class T>
 void launch_dx(const DxArgs& a, dim3 g, hipStream_t stream) {
@@ -521,16 +539,18 @@ int weight_gradient(DwArgs<T> a, float* part, hipStream_t stream) {
         k_dw<Mid, T><<<g, Mid::kThreads, 0, stream>>>(a);
     } else {
         const int64_t kp = padded(a.k, 4);
-        const DwArgs<float> p{a.dy, a.x, a.ld, a.cols, a.cols, a.ldx, {part, part}, a.m, a.cols, kp, a.ni, a.nj, a.steps};
+        const DwArgs<float> p{a.dy, a.x,    a.ld, a.cols, a.cols, a.ldx,  {part, part},
+                              a.m,  a.cols, kp,   a.ni,   a.nj,   a.steps};
         k_dw<Mid, float><<<g, Mid::kThreads, 0, stream>>>(p);
-        k_join<<<fqh::grid_all(a.cols * kp / 4, 256), 256, 0, stream>>>(part, (int)c.splits, a.cols, a.n, a.run, (uint32_t)a.k,
-                                                                        (uint32_t)kp, a.dw[0], a.dw[1]);
+        k_join<<<fqh::grid_all(a.cols * kp / 4, 256), 256, 0, stream>>>(
+            part, (int)c.splits, a.cols, a.n, a.run, (uint32_t)a.k, (uint32_t)kp, a.dw[0], a.dw[1]);
     }
     return fqh::launched();
 }
 
-int products(const DxArgs& dx, const uint16_t* dy, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype, void* part,
-             hipStream_t stream) {
+// dx from dx.dy, the weights' gradients from dy (the same values, in bfloat16).
+int products(const DxArgs& dx, const uint16_t* dy, const uint16_t* x, int64_t ldx, void* dw, void* dw2, int dw_dtype,
+             void* part, hipStream_t stream) {
     if (dx.dx) {
         const int st = input_gradient(dx, (float*)part, stream);
         if (st != FQ_OK || !dw) return st;
@@ -559,8 +579,8 @@ int matmul_backward(const void* dy, const void* x, int64_t m, int64_t n, int64_t
     const uint16_t* xs = dw ? chunk_rows(x, m, k, at, stream) : nullptr;
     const W4Mat wm = dx ? w4_mat(*w, k, group) : W4Mat{};
     const int64_t ld = padded(n, 8);
-    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, dx, m, n, k}, y, xs, padded(k, 8), dw, nullptr, dw_dtype, at,
-                    stream);
+    return products({y, ld, ld, padded(n, kDeep), {wm, wm}, dx, m, n, k}, y, xs, padded(k, 8), dw, nullptr, dw_dtype,
+                    at, stream);
 }
 
 int gated_backward(const void* dh, const void* x, const void* g, const void* u, int64_t m, int64_t n, int64_t k,
@@ -572,9 +592,10 @@ int gated_backward(const void* dh, const void* x, const void* g, const void* u, 
     int32_t* shift = (int32_t*)(down + 2 * run);
     char* at = (char*)(shift + padded(m, 4));
     if (dx)
-        k_row_powers<<<(unsigned)((2 * run + 15) / 16), 256, 0, stream>>>(gate->scale, up->scale, n, run, ng, up_by, down);
-    k_gate_grad<<<(unsigned)m, 512, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, act, n, run,
-                                                 up_by, dx ? half : nullptr, shift, dw_gate ? both : nullptr);
+        k_row_powers<<<(unsigned)((2 * run + 15) / 16), 256, 0, stream>>>(gate->scale, up->scale, n, run, ng, up_by,
+                                                                          down);
+    k_gate_grad<<<(unsigned)m, 512, 0, stream>>>((const uint16_t*)dh, (const uint16_t*)g, (const uint16_t*)u, act, n,
+                                                 run, up_by, dx ? half : nullptr, shift, dw_gate ? both : nullptr);
     const uint16_t* xs = dw_gate ? chunk_rows(x, m, k, at, stream) : nullptr;
     DxArgs a{half, 2 * run, 2 * run, run, {}, dx, m, n, k, 0, 0, 0, shift, down};
     if (dx) a.w[0] = w4_mat(*gate, k, group), a.w[1] = w4_mat(*up, k, group);

@@ -305,9 +305,14 @@ int few(const FewArgs<T>& a, int64_t group, hipStream_t stream) {
     // 32 rows 13.3 us, by 16 18.9, by 64 20.0; 64 float32 tokens, 4096 x 4096: 8 x 4 tokens by
     // 32 rows 19.4 us, by 16 30.7; 24 tokens there: 8 x 4 tokens 8.4 us, 16 x 4 11.4.
     if (a.m <= 4) return launch<T, 1, 1, W, 4>(a, group, stream);
-    if constexpr (sizeof(T) == 4) return a.m <= 16 ? launch<T, 4, 1, W, 1>(a, group, stream) : launch<T, 8, 2 / W, W, 1>(a, group, stream);
-    if (a.m <= 16) return launch<T, 4, 1, W, 2>(a, group, stream);
-    return a.m <= 32 ? launch<T, 8, 2 / W, W, 1>(a, group, stream) : launch<T, 16, 2 / W, W, 1>(a, group, stream);
+    if constexpr (sizeof(T) == 4) {
+        if (a.m <= 16) return launch<T, 4, 1, W, 1>(a, group, stream);
+        return launch<T, 8, 2 / W, W, 1>(a, group, stream);
+    } else {
+        if (a.m <= 16) return launch<T, 4, 1, W, 2>(a, group, stream);
+        if (a.m <= 32) return launch<T, 8, 2 / W, W, 1>(a, group, stream);
+        return launch<T, 16, 2 / W, W, 1>(a, group, stream);
+    }
 }
 
 }  // namespace
@@ -322,10 +327,12 @@ int few_matmul(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_
 int few_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int64_t group, int act, const fql_w4& gate,
               const fql_w4& up, void* h, void* g, void* u, hipStream_t stream) {
     const W4Mat wg = w4_mat(gate, k, group), wu = w4_mat(up, k, group);
-    if (dtype == FQ_F32)
-        return few<float, 2>({(const float*)x, {wg, wu}, {(float*)h, (float*)g, (float*)u}, m, n, k, 0, 0, act}, group, stream);
-    return few<uint16_t, 2>({(const uint16_t*)x, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k, 0, 0, act},
-                            group, stream);
+    if (dtype == FQ_F32) {
+        const FewArgs<float> a{(const float*)x, {wg, wu}, {(float*)h, (float*)g, (float*)u}, m, n, k, 0, 0, act};
+        return few<float, 2>(a, group, stream);
+    }
+    const FewArgs<uint16_t> a{(const uint16_t*)x, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k, 0, 0, act};
+    return few<uint16_t, 2>(a, group, stream);
 }
 
 }  // namespace fqw

@@ -55,7 +55,8 @@ struct CodeRows {
     int row, half;
     template <class Args>
     __device__ __forceinline__ CodeRows(const Args& a, int64_t col0, int t)
-        : spans(a.spans), inverse(a.inverse), parts(a.parts), steps((uint32_t)((a.k + kDeep - 1) / kDeep)), row(t / 2), half(t % 2) {
+        : spans(a.spans), inverse(a.inverse), parts(a.parts), steps((uint32_t)((a.k + kDeep - 1) / kDeep)), row(t / 2),
+          half(t % 2) {
         // a wave's 64 rows of the tile hold 32 of the gate matrix and then the same 32 of the up matrix
         const int which = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(row / 32 % 2);
         const W4Mat& w = a.w[which];
@@ -287,7 +288,8 @@ int forward(ForwardArgs<T> a, const T* x, int64_t group, void* workspace, hipStr
     }
     using Big = Shape<256, 256, 2, 4>;
     using Mid = Shape<128, 256, 2, 4>;
-    if (big_tiles(a.m, a.n * W)) return fine ? launch<Big, 32, W, T>(a, zp, stream) : launch<Big, 64, W, T>(a, zp, stream);
+    if (big_tiles(a.m, a.n * W))
+        return fine ? launch<Big, 32, W, T>(a, zp, stream) : launch<Big, 64, W, T>(a, zp, stream);
     return fine ? launch<Mid, 32, W, T>(a, zp, stream) : launch<Mid, 64, W, T>(a, zp, stream);
 }
 
@@ -317,7 +319,8 @@ int forward_gated(const void* x, int dtype, int64_t m, int64_t n, int64_t k, int
         ForwardArgs<float> a{nullptr, 0, 0, 0, {wg, wu}, {(float*)h, (float*)g, (float*)u}, m, n, k, 0, 0, 0, 0, act};
         return forward<2, float>(a, (const float*)x, group, workspace, stream);
     }
-    ForwardArgs<uint16_t> a{nullptr, 0, 0, 0, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k, 0, 0, 0, 0, act};
+    ForwardArgs<uint16_t> a{nullptr, 0, 0, 0, {wg, wu}, {(uint16_t*)h, (uint16_t*)g, (uint16_t*)u}, m, n, k,
+                            0,       0, 0, 0, act};
     return forward<2, uint16_t>(a, (const uint16_t*)x, group, workspace, stream);
 }
 

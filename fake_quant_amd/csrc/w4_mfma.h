@@ -162,7 +162,8 @@ struct Tokens<float> {
             float r[2], s[2], h[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                h[j] = __builtin_canonicalizef(__uint_as_float(v[i / 2][2 * (i % 2) + j]));  // a NaN keeps a bit in its upper half
+                // a NaN keeps a bit in its upper half
+                h[j] = __builtin_canonicalizef(__uint_as_float(v[i / 2][2 * (i % 2) + j]));
                 const float top = __uint_as_float(__float_as_uint(h[j]) & 0xFFFF0000u);
                 r[j] = fabsf(h[j]) < INFINITY ? h[j] - top : 0.0f;
                 s[j] = r[j] - __uint_as_float(__float_as_uint(r[j]) & 0xFFFF0000u);
