@@ -13,7 +13,7 @@
 // 1.0 PFLOP/s (decoding before the products 145), dw 115 .. 121 us, 1.15 PFLOP/s, the matrix
 // units busy for 65 % at 2.0 GHz (a step's operands read at its start, a buffer descriptor
 // for each load: 125).  Gated block, 4096 tokens, 12288 x 4096: dg and du 150 us (4.6 TB/s),
-// dx 860 .. 890, dw 690.
+// dx 800 .. 850 (64-bit offsets per thread: 890), dw 690.
 #include "fq_host.h"
 #include "w4_linear.h"
 #include "w4_tile.h"
